@@ -45,11 +45,11 @@ def listed():
         # a long prompt: some hundred rows for each expert, unevenly spread
         {"name": "swiglu prompt", "op": "swiglu", "T": 8192, "E": 256, "k": 8, "K": 7168, "N": 2048, "skew": 0.5, "quant": "fp8"},
         # the smallest product: one token's eight down projections
-        {"name": "gemm decode", "op": "gemm", "T": 1, "E": 256, "k": 8, "K": 2048, "N": 7168, "skew": 0.0, "quant": "fp8", "gather": False, "f32": False},
-        # MXFP8 latents through one GPU's share of experts, rows gathered, sums kept in FP32
-        {"name": "gemm latent mxfp8", "op": "gemm", "T": 1237, "E": 56, "k": 2, "K": 3584, "N": 2048, "skew": 0.5, "quant": "mxfp8", "gather": True, "f32": True},
+        {"name": "gemm decode", "op": "gemm", "T": 1, "E": 256, "k": 8, "K": 2048, "N": 7168, "skew": 0.0, "quant": "fp8", "gather": False},
+        # MXFP8 latents through one GPU's share of experts, rows gathered
+        {"name": "gemm latent mxfp8", "op": "gemm", "T": 1237, "E": 56, "k": 2, "K": 3584, "N": 2048, "skew": 0.5, "quant": "mxfp8", "gather": True},
         # a long prompt's down projection
-        {"name": "gemm prompt", "op": "gemm", "T": 8192, "E": 256, "k": 8, "K": 2048, "N": 7168, "skew": 0.5, "quant": "fp8", "gather": False, "f32": False},
+        {"name": "gemm prompt", "op": "gemm", "T": 8192, "E": 256, "k": 8, "K": 2048, "N": 7168, "skew": 0.5, "quant": "fp8", "gather": False},
     ]
 
 
@@ -72,7 +72,7 @@ def draw(rng):
             "N": 128 * _log(rng, 2, 16 if op == "swiglu" else 56), "skew": rng.choice([0.0, 0.5, 1.0]), "quant": rng.choice(["fp8", "fp8", "mxfp8"])}
     if op == "gemm":
         case["N"] = min(case["N"], 128 * (7168 * 2048 // 128 // case["K"]))  # no expert larger than the listed ones
-        case["gather"], case["f32"] = rng.random() < 0.5, rng.random() < 0.3
+        case["gather"] = rng.random() < 0.5
     return case
 
 
@@ -246,8 +246,7 @@ def _plain_swiglu(s):
 
 
 def _plain_gemm(s):
-    y = _plain_products(s)
-    return {"y": y if s["case"]["f32"] else y.to(torch.bfloat16)}
+    return {"y": _plain_products(s).to(torch.bfloat16)}
 
 
 # ---- the framework's calls ----------------------------------------------------------------------
@@ -280,8 +279,7 @@ def _own_swiglu(s):
 def _own_gemm(s):
     import fp8_block_scaled_moe_amd as moe
 
-    return {"y": moe.grouped_gemm(s["x"], s["x_scale"], s["w"], s["w_scale"], s["offsets"], rows=s["rows"],
-                                  out_dtype=torch.float32 if s["case"]["f32"] else torch.bfloat16)}
+    return {"y": moe.grouped_gemm(s["x"], s["x_scale"], s["w"], s["w_scale"], s["offsets"], rows=s["rows"])}
 
 
 def run(state):
@@ -309,7 +307,7 @@ def work(case):
     touched = E * (1.0 - (1.0 - k / E) ** T)  # experts that some token picks, on average
     tokens = T if c["op"] == "swiglu" or c["gather"] else R
     read = touched * (N * K + N * K // 4096) + tokens * (K + K // 32) + R * 4 + E * 4
-    wrote = R * c["N"] * (1 + 1 / 32 if c["op"] == "swiglu" else 4 if c["f32"] else 2)
+    wrote = R * c["N"] * (1 + 1 / 32 if c["op"] == "swiglu" else 2)
     return {"bytes": read + wrote, "flops": 2.0 * R * N * K}
 
 
