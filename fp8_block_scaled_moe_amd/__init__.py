@@ -1,9 +1,8 @@
 """Routed-expert FP8 block-scaled MoE decode for MI355X (gfx950).
 
 The compute path is the HIP library libmoe_decode.so (C ABI in
-include/moe_decode.h and include/moe_boundary.h); this package is its thin
-Python binding. Build the
-library with `python -m fp8_block_scaled_moe_amd.build`.
+include/moe_decode.h, include/moe_boundary.h and include/moe_rows.h); this
+package is its thin Python binding. Build the library with `python -m fp8_block_scaled_moe_amd.build`.
 """
 
 from ._capi import (  # noqa: F401
@@ -17,4 +16,11 @@ from ._capi import (  # noqa: F401
     lib,
     mxfp8_quantize,
     reduce_rmsnorm,
+)
+from ._rows import (  # noqa: F401
+    RoutedRows,
+    add_rmsnorm_quant,
+    grouped_gemm,
+    grouped_swiglu,
+    route_rows,
 )

@@ -134,6 +134,11 @@ def lib() -> ctypes.CDLL:
     L.moe_mxfp8_quantize.restype = ctypes.c_int
     L.moe_reduce_rmsnorm.argtypes = [vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, vp]
     L.moe_reduce_rmsnorm.restype = ctypes.c_int
+    for name in ("moe_add_rmsnorm_quant", "moe_route_rows", "moe_grouped_gemm", "moe_grouped_swiglu"):
+        getattr(L, name).argtypes = [vp, vp]
+        getattr(L, name).restype = ctypes.c_int
+    L.moe_route_rows_workspace.argtypes = [i32, i32]
+    L.moe_route_rows_workspace.restype = sz
     _lib = L
     return L
 

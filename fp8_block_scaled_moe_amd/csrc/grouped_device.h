@@ -1,0 +1,163 @@
+// Device pieces shared by the grouped products (moe_rows.h): which rows a
+// workgroup has, where an activation row lies, and the block product.
+#pragma once
+
+#include "rows_device.h"
+
+namespace moe {
+
+struct GroupedArgs {
+  const uint8_t* x;
+  const void* xs;
+  const int32_t* rows;
+  const int32_t* offsets;
+  const uint8_t* w;
+  const float* ws;
+  void* out;
+  float* outs;
+  int R, X, E, N, K;
+  float limit;
+  int col_tiles;  // column tiles of an expert's output
+};
+
+// A workgroup's tile: expert e, grouped rows [row, end) of which it takes the
+// first ones, column tile `col`. e < 0: no tile is left for it.
+struct TileAt {
+  int e, row, end, col;
+};
+
+// The workgroup's tile when every expert's rows are cut into tiles of kRows.
+// The row tiles are counted anew by every workgroup (offsets are on the
+// device; E + 1 of them from L2 and one sum over the workgroup, about 1 us).
+// Tiles are numbered expert by expert, inside an expert column tile by column
+// tile, the expert's row tiles fastest, so that neighbours share weights; and
+// each XCD (workgroup id mod 8) takes a contiguous eighth of the numbers, so
+// that what neighbours share meets in one L2. Every thread calls it; barriers
+// inside.
+template <int kRows, int kThreadsWg>
+__device__ __forceinline__ TileAt find_tile(const GroupedArgs& a, int block) {
+  constexpr int kWavesWg = kThreadsWg / kWave;
+  constexpr int kPer = 1024 / kThreadsWg;  // experts per thread: E <= 1024
+  static_assert(kPer >= 1, "every expert has a thread");
+  __shared__ int wave_sum[kWavesWg];
+  __shared__ int found[4];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int per = (a.E + kThreadsWg - 1) / kThreadsWg;
+  const auto clamped = [&](int e) { return min(max(a.offsets[min(e, a.E)], 0), a.R); };
+  int lo[kPer], tiles[kPer], sum = 0;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int e = tid * per + q;
+    lo[q] = tiles[q] = 0;
+    if (q < per && e < a.E) {
+      lo[q] = clamped(e);
+      tiles[q] = (max(clamped(e + 1) - lo[q], 0) + kRows - 1) / kRows;
+    }
+    sum += tiles[q];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int up = __shfl_up(incl, o, kWave);
+    incl += lane >= o ? up : 0;
+  }
+  if (lane == kWave - 1) wave_sum[wave] = incl;
+  if (tid == 0) found[0] = -1;
+  __syncthreads();
+  int before = incl - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWavesWg; ++w) {
+    before += w < wave ? wave_sum[w] : 0;
+    total += wave_sum[w];
+  }
+  const int64_t all = (int64_t)total * a.col_tiles;
+  const int64_t share = (all + 7) / 8;
+  const int64_t at = (int64_t)(block & 7) * share + (block >> 3);
+  if ((block >> 3) < share && at < all) {
+    const int t = (int)(at / a.col_tiles);  // lies in its expert's range of row tiles
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      if (t >= before && t < before + tiles[q]) {
+        const int mine = (int)(at - (int64_t)before * a.col_tiles);
+        found[0] = tid * per + q;
+        found[1] = lo[q] + (mine % tiles[q]) * kRows;
+        found[2] = clamped(tid * per + q + 1);
+        found[3] = mine / tiles[q];
+      }
+      before += tiles[q];
+    }
+  }
+  __syncthreads();
+  TileAt r;
+  r.e = __builtin_amdgcn_readfirstlane(found[0]);
+  r.row = __builtin_amdgcn_readfirstlane(found[1]);
+  r.end = __builtin_amdgcn_readfirstlane(found[2]);
+  r.col = __builtin_amdgcn_readfirstlane(found[3]);
+  return r;
+}
+
+// The activation row of grouped row i, -1 where its index is out of range.
+__device__ __forceinline__ int x_row(const GroupedArgs& a, int i) {
+  const int r = a.rows ? a.rows[i] : i;
+  return r >= 0 && r < a.X ? r : -1;
+}
+
+// Lane l = 16 g + r of a 128-wide K block holds bytes 16g .. 16g+15 (lo) and
+// 64+16g .. 64+16g+15 (hi) of row r: the register layout of the 16x16x128 FP8
+// instruction, used for weights and activations alike.
+
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+
+// Eight e4m3 codes as F16 values times a power of two.
+__device__ __forceinline__ half8_t widen8_scaled(uint32_t w0, uint32_t w1, float scale) {
+  const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, scale, false);
+  const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, scale, true);
+  const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, scale, false);
+  const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, scale, true);
+  return half8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// A lane's 32 codes of a block as F16: exact, or times a power of two for
+// each half.
+struct Wide {
+  half8_t v[4];
+};
+__device__ __forceinline__ Wide widen(const u32x4_t& lo, const u32x4_t& hi, float slo = 1.f, float shi = 1.f) {
+  return Wide{{widen8_scaled(lo[0], lo[1], slo), widen8_scaled(lo[2], lo[3], slo), widen8_scaled(hi[0], hi[1], shi),
+               widen8_scaled(hi[2], hi[3], shi)}};
+}
+
+// The 16 x 16 products of a block, exact F16 products summed in FP32: lane
+// 16 g + r gets activation row r by weight rows 4g .. 4g+3.
+__device__ __forceinline__ float4_t product_f16(const Wide& w, const Wide& x) {
+  float4_t p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.v[i], x.v[i], p, 0, 0, 0);
+  return p;
+}
+
+// Scales of a lane's two halves under MXFP8, from its row's four E8M0 bytes
+// of a block (32 positions each): the largest byte as the block's own scale,
+// the others relative to it, which keeps every product inside F16 (an element
+// 2^15 and more below the largest block's loses bits that lie below an FP32
+// sum's).
+struct MxScales {
+  float lo, hi, block;
+};
+__device__ __forceinline__ MxScales mx_scales(uint32_t bytes, int g) {
+  const auto byte = [&](int b) { return (int)((bytes >> (8 * b)) & 0xFFu); };
+  const int top = max(max(byte(0), byte(1)), max(byte(2), byte(3)));
+  const auto rel = [&](int b) { return __uint_as_float((uint32_t)max(127 + byte(b) - top, 1) << 23); };
+  const bool odd = g >= 2;  // bytes 16g .. 16g+15 lie in block g / 2, 64 further in block 2 + g / 2
+  return MxScales{rel(odd ? 1 : 0), rel(odd ? 3 : 2), __uint_as_float(top ? (uint32_t)top << 23 : 0x400000u)};
+}
+
+// gate / (1 + exp(-gate)) * up with both clamped. A clamped NaN stays one.
+__device__ __forceinline__ float swiglu(float up, float gate, float limit) {
+  up = up != up ? up : __builtin_amdgcn_fmed3f(up, -limit, limit);
+  gate = gate > limit ? limit : gate;
+  const float e = __builtin_amdgcn_exp2f(gate * -1.44269504088896341f);
+  return gate * __builtin_amdgcn_rcpf(1.f + e) * up;
+}
+
+}  // namespace moe

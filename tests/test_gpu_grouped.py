@@ -1,0 +1,302 @@
+"""moe_grouped_gemm and moe_grouped_swiglu on the GPU against the formula in
+64 bits (torch FP64 products per expert; the inputs are e4m3 codes and
+binary32 scales, exact in FP64).
+
+Bound of the product: a 128-wide block's exact products are added in FP32 (at
+most 127 additions in some order), its scales are applied in at most three
+FP32 operations, and the K/128 partials are added in FP32. With an error of
+one unit 2^-23 each (either rounding or truncation), the result is within
+(128 + K/128 + 3) * 2^-23 * sum |terms| of the exact one. A BF16 output is the
+rounding of such a value: between the roundings of exact -+ bound."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from fp8_block_scaled_moe_amd import grouped_gemm, grouped_swiglu
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+F8 = torch.float8_e4m3fn
+LIMIT = 7.0
+
+
+def codes(gen, shape, std):
+    return (torch.randn(shape, generator=gen, device=DEV) * std).clamp(-448, 448).to(F8)
+
+
+def make(counts, N, K, seed, quant="fp8", gather=False, std=107.0, extra=3):
+    """Inputs for experts with these row counts; with gather the rows are
+    drawn, with repeats, from fewer tokens; `extra` rows lie behind the last."""
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    E, R = len(counts), sum(counts)
+    X = max(1, R // 2 + 1) if gather else R + extra
+    d = {"w": codes(gen, (E, N, K), std), "w_scale": torch.rand(E, N // 128, K // 128, generator=gen, device=DEV) * 1.5 + 0.5}
+    d["w_scale"] /= std * K**0.5
+    d["x"] = codes(gen, (X, K), 100.0)
+    if quant == "fp8":
+        d["x_scale"] = torch.exp2(torch.randn(X, K // 128, generator=gen, device=DEV)) / 100.0
+    else:
+        d["x_scale"] = torch.randint(115, 125, (X, K // 32), generator=gen, device=DEV).to(torch.uint8)
+    d["offsets"] = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device=DEV)
+    d["rows"] = torch.randint(0, X, (R + extra,), generator=gen, device=DEV, dtype=torch.int32) if gather else None
+    return d
+
+
+def exact(d):
+    """(g, sum of |terms|) in FP64 for the rows up to offsets[-1]."""
+    ends = d["offsets"].tolist()
+    K = d["x"].shape[1]
+    x = d["x"].double()
+    if d["x_scale"].dtype == torch.uint8:
+        x = x * torch.exp2(d["x_scale"].double() - 127).repeat_interleave(32, 1)
+    else:
+        x = x * d["x_scale"].double().repeat_interleave(128, 1)
+    if d["rows"] is not None:
+        ok = (d["rows"] >= 0) & (d["rows"] < x.shape[0])
+        x = torch.where(ok[:, None], x[d["rows"].long().clamp(0, x.shape[0] - 1)], torch.zeros((), dtype=torch.float64, device=DEV))
+    g = torch.zeros(ends[-1], d["w"].shape[1], dtype=torch.float64, device=DEV)
+    t = torch.zeros_like(g)
+    for e in range(len(ends) - 1):
+        lo, hi = ends[e], ends[e + 1]
+        if hi > lo:
+            w = d["w"][e].double() * d["w_scale"][e].double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+            g[lo:hi] = x[lo:hi] @ w.t()
+            t[lo:hi] = x[lo:hi].abs() @ w.abs().t()
+    return g, t * ((128 + K // 128 + 3) * 2.0**-23)
+
+
+def call_gemm(d):
+    return grouped_gemm(d["x"], d["x_scale"], d["w"], d["w_scale"], d["offsets"], rows=d["rows"])
+
+
+def check_gemm(d, more=0.0):
+    y = call_gemm(d)
+    g, bound = exact(d)
+    n = g.shape[0]
+    got = y[:n].double()
+    # a value within the bound, rounded once; BF16 rounding is monotone
+    bf16 = lambda v: v.float().to(torch.bfloat16).double()  # noqa: E731
+    bad = (got < bf16(g - bound - more)) | (got > bf16(g + bound + more))
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} values outside, first at {torch.nonzero(bad)[0].tolist()}"
+    return y
+
+
+def check_swiglu(d):
+    h, s = grouped_swiglu(d["x"], d["x_scale"], d["w"], d["w_scale"], d["offsets"], limit=LIMIT, rows=d["rows"])
+    g, bound = exact(d)
+    n, I = g.shape[0], g.shape[1] // 2
+    up, gate = g[:, :I].clamp(-LIMIT, LIMIT), g[:, I:].clamp_max(LIMIT)
+    silu = gate * torch.sigmoid(gate)
+    act = silu * up
+    # |silu'| < 1.1; the hardware's exp2 and reciprocal and the FP32 steps
+    # around them: |gate| + 4 units of 2^-23
+    err = 1.1 * bound[:, I:] * up.abs() + (silu.abs() + 1.1 * bound[:, I:]) * bound[:, :I] + act.abs() * (gate.abs() + 4) * 2.0**-23
+    block = lambda v: v.view(n, I // 128, 128).amax(-1)  # noqa: E731
+    sg = s[:n].double()
+    ws = block(act.abs()).clamp_min(1e-10) / 448.0
+    assert ((sg - ws).abs() <= block(err) / 448.0 + ws * 2.0**-23).all(), "scales"
+    # the code is the rounding of a value within the error of act / scale
+    # (scale as returned; its reciprocal and the product round once each)
+    spread = sg.repeat_interleave(128, 1)
+    e = err + act.abs() * 2.0**-22
+    f8 = lambda v: v.clamp(-448, 448).float().to(F8).double()  # noqa: E731
+    lo, hi = f8((act - e) / spread), f8((act + e) / spread)
+    got = h[:n].view(F8).double()
+    bad = (got < lo) | (got > hi)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} codes outside, first at {torch.nonzero(bad)[0].tolist()}"
+    return h, s
+
+
+RAGGED = [0, 1, 15, 16, 17, 0, 63, 64, 65, 2]
+BIG = [127, 128, 129, 0, 255, 256, 257, 300, 1, 513]
+
+
+@pytest.mark.parametrize("quant", ["fp8", "mxfp8"])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0, 5], RAGGED, BIG, [0, 0, 700]], ids=["one", "few", "ragged", "big", "last"])
+def test_gemm_counts(counts, gather, quant):
+    check_gemm(make(counts, 384, 640, 1, quant, gather))
+
+
+@pytest.mark.parametrize("quant", ["fp8", "mxfp8"])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0, 5], RAGGED, BIG, [0, 0, 700]], ids=["one", "few", "ragged", "big", "last"])
+def test_swiglu_counts(counts, gather, quant):
+    check_swiglu(make(counts, 768, 640, 2, quant, gather))
+
+
+@pytest.mark.parametrize("N,K", [(128, 128), (128, 256), (256, 384), (640, 128), (1408, 1408), (256, 7168), (7168, 256), (512, 16384)])
+@pytest.mark.parametrize("counts", [[2, 0, 1], [5, 40, 9], [150, 30, 290]], ids=["few", "some", "many"])
+def test_gemm_sizes(N, K, counts):
+    check_gemm(make(counts, N, K, 3))
+
+
+@pytest.mark.parametrize("I,K", [(128, 128), (128, 512), (384, 256), (1408, 1408), (256, 7168), (2048, 256)])
+@pytest.mark.parametrize("counts", [[2, 0, 1], [5, 40, 9], [150, 30, 290]], ids=["few", "some", "many"])
+def test_swiglu_sizes(I, K, counts):
+    check_swiglu(make(counts, 2 * I, K, 4))
+
+
+@pytest.mark.parametrize("E,R", [(1, 1), (1, 1000), (256, 40), (300, 2000), (1024, 100), (1024, 5000), (257, 20000)])
+def test_many_experts(E, R):
+    counts = np.bincount(np.random.default_rng(E + R).integers(0, E, R), minlength=E).tolist()
+    check_gemm(make(counts, 256, 256, 5, gather=True))
+    check_swiglu(make(counts, 256, 256, 6, gather=True))
+
+
+def test_exact_integers():
+    """Small integers and power-of-two scales: every sum is exact in FP32, so
+    the output has to be the exact value's BF16 rounding, whichever order it
+    is summed in."""
+    for counts in ([3, 0, 20], [100, 260]):
+        for quant in ("fp8", "mxfp8"):
+            d = make(counts, 256, 512, 7, quant)
+            gen = torch.Generator(device=DEV).manual_seed(8)
+            d["x"] = torch.randint(-7, 8, d["x"].shape, generator=gen, device=DEV).float().to(F8)
+            d["w"] = torch.randint(-7, 8, d["w"].shape, generator=gen, device=DEV).float().to(F8)
+            d["w_scale"] = torch.exp2(torch.randint(-2, 3, d["w_scale"].shape, generator=gen, device=DEV).float())
+            if quant == "fp8":
+                d["x_scale"] = torch.exp2(torch.randint(-2, 3, d["x_scale"].shape, generator=gen, device=DEV).float())
+            else:
+                d["x_scale"] = torch.randint(125, 130, d["x_scale"].shape, generator=gen, device=DEV).to(torch.uint8)
+            assert torch.equal(call_gemm(d)[: sum(counts)], exact(d)[0].float().to(torch.bfloat16))
+
+
+def test_every_code():
+    """All finite e4m3 codes in x and w, subnormals among them."""
+    d = make([40, 3], 256, 512, 9)
+    finite = torch.tensor([c for c in range(256) if c & 0x7F != 0x7F], dtype=torch.uint8, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(10)
+    for n in ("x", "w"):
+        d[n] = finite[torch.randint(0, 254, d[n].shape, generator=gen, device=DEV)].view(F8)
+    check_gemm(d)
+
+
+def test_e8m0_range():
+    """E8M0 bytes over the range whose products stay finite, 0 included."""
+    d = make([20, 100], 256, 512, 11, "mxfp8")
+    gen = torch.Generator(device=DEV).manual_seed(12)
+    d["x_scale"] = torch.randint(0, 200, d["x_scale"].shape, generator=gen, device=DEV).to(torch.uint8)
+    d["x_scale"][0, :] = 0
+    d["w_scale"][:] = 1.0
+    check_gemm(d, 2.0**-126)  # results below the smallest normal may be flushed
+
+
+@pytest.mark.parametrize("counts", [[3, 1], [40, 30], [300, 200]], ids=["few", "some", "many"])
+def test_rows_behind_the_last_stay(counts):
+    """Rows of the output from offsets[E] on are left as they were."""
+    import ctypes
+    from fp8_block_scaled_moe_amd import _rows, lib
+
+    d = make(counts, 256, 256, 13, extra=50)
+    R, n = d["x"].shape[0], sum(counts)
+    st = torch.cuda.current_stream().cuda_stream
+    sizes = (R, R, len(counts), 256, 256, 1)
+    ptrs = (d["x"].data_ptr(), d["x_scale"].data_ptr(), None, d["offsets"].data_ptr(), d["w"].data_ptr(), d["w_scale"].data_ptr())
+    out = torch.full((R, 256), 3.0, dtype=torch.bfloat16, device=DEV)
+    assert lib().moe_grouped_gemm(ctypes.byref(_rows.GroupedArgs(*sizes, 0.0, *ptrs, out.data_ptr(), None)), st) == 0
+    assert (out[n:] == 3.0).all() and torch.equal(out[:n], call_gemm(d)[:n])
+    h, s = torch.full((R, 128), 9, dtype=torch.uint8, device=DEV), torch.full((R, 1), 5.0, device=DEV)
+    a = _rows.GroupedArgs(*sizes, LIMIT, *ptrs, h.data_ptr(), s.data_ptr())
+    assert lib().moe_grouped_swiglu(ctypes.byref(a), st) == 0
+    assert (h[n:] == 9).all() and (s[n:] == 5.0).all()
+
+
+@pytest.mark.parametrize("counts", [[4, 2], [40, 30], [300, 200]], ids=["few", "some", "many"])
+def test_rows_outside_give_zeros(counts):
+    d = make(counts, 256, 256, 14, gather=True, extra=0)
+    d["rows"][1], d["rows"][-1], d["rows"][2] = -1, d["x"].shape[0], -(2**31)
+    y = check_gemm(d)
+    assert not y[[1, 2, -1]].any()
+    h, s = check_swiglu(d)
+    assert not h[[1, 2, -1]].any()
+
+
+@pytest.mark.parametrize("counts", [[4, 2], [40, 30], [300, 200]], ids=["few", "some", "many"])
+def test_offsets_outside_are_clamped(counts):
+    """Offsets past R or below 0 end at R or begin at 0."""
+    d = make(counts, 256, 256, 15, extra=0)
+    want = call_gemm(d)
+    d["offsets"][0], d["offsets"][-1] = -5, 2**31 - 1
+    assert torch.equal(call_gemm(d), want)
+
+
+@pytest.mark.parametrize("counts", [[4, 2], [40, 30], [300, 200]], ids=["few", "some", "many"])
+def test_nan_stays_in_its_row(counts):
+    """A NaN code in a row of x, or in another expert's weights, reaches only
+    the rows that contain it."""
+    d = make(counts, 256, 256, 16, extra=0)
+    want_y, want_h = call_gemm(d), check_swiglu(d)
+    d["x"].view(torch.uint8)[1, 77] = 0x7F
+    y = call_gemm(d)
+    keep = torch.arange(y.shape[0], device=DEV) != 1
+    assert torch.isnan(y[1]).all() and torch.equal(y[keep], want_y[keep])
+    h, s = grouped_swiglu(d["x"], d["x_scale"], d["w"], d["w_scale"], d["offsets"], limit=LIMIT)
+    assert ((h[1] & 0x7F) == 0x7F).all() and torch.equal(h[keep], want_h[0][keep]) and torch.equal(s[keep], want_h[1][keep])
+    d = make(counts, 256, 256, 16, extra=0)
+    d["w"].view(torch.uint8)[1, 200, 100] = 0xFF
+    y = call_gemm(d)
+    assert torch.isnan(y[counts[0] :, 200]).all()
+    assert torch.equal(y[: counts[0]], want_y[: counts[0]])
+    cols = torch.arange(256, device=DEV) != 200
+    assert torch.equal(y[:, cols], want_y[:, cols])
+
+
+def test_saturated_swiglu():
+    """Large products: both clamps act, a very negative gate gives zero."""
+    for counts in ([3, 2], [300, 200]):
+        d = make(counts, 512, 256, 17)
+        d["w_scale"] *= 1000.0
+        check_swiglu(d)
+
+
+def test_zero_inputs():
+    d = make([2, 0, 40], 256, 256, 18)
+    d["x"] = torch.zeros_like(d["x"].view(torch.uint8)).view(F8)
+    assert not call_gemm(d)[:42].any()
+    h, s = check_swiglu(d)
+    assert not h[:42].any() and torch.equal(s[:42], torch.full_like(s[:42], np.float32(1e-10) / np.float32(448.0)))
+
+
+def test_empty():
+    d = make([1], 256, 256, 19, extra=0)
+    d["x"], d["x_scale"] = d["x"][:0], d["x_scale"][:0]
+    d["offsets"].zero_()
+    assert call_gemm(d).shape == (0, 256)
+    h, s = grouped_swiglu(d["x"], d["x_scale"], d["w"], d["w_scale"], d["offsets"], limit=LIMIT)
+    assert h.shape == (0, 128) and s.shape == (0, 1)
+    d = make([3, 2], 256, 256, 20)  # rows, but none of them grouped
+    d["offsets"].zero_()
+    call_gemm(d)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("counts", [[4, 2], [40, 30], [300, 200]], ids=["few", "some", "many"])
+def test_same_bits_every_time_and_wherever_a_row_stands(counts):
+    """No order-dependent sums: a repeated call is bit-identical, and a row's
+    result does not depend on its place among the rows of its expert."""
+    d = make(counts, 512, 640, 21, extra=0)
+    a, b = call_gemm(d), call_gemm(d)
+    assert torch.equal(a, b)
+    d["rows"] = torch.cat([torch.arange(counts[0]).flip(0), counts[0] + torch.arange(counts[1]).flip(0)]).int().to(DEV)
+    assert torch.equal(call_gemm(d)[d["rows"].long()], a)
+
+
+def test_weights_past_32_bits():
+    """Expert offsets past 4 GiB: the last of 300 experts of 2048 x 7168."""
+    E, N, K = 300, 2048, 7168
+    big = make([6], N, K, 23, extra=0)
+    w = torch.zeros(E, N, K, dtype=torch.uint8, device=DEV)
+    w[-1] = big["w"][0].view(torch.uint8)
+    ws = torch.zeros(E, N // 128, K // 128, device=DEV)
+    ws[-1] = big["w_scale"][0]
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    offsets[-1] = 6
+    y = grouped_gemm(big["x"], big["x_scale"], w, ws, offsets)
+    g, bound = exact(big)
+    bf16 = lambda v: v.float().to(torch.bfloat16).double()  # noqa: E731
+    assert ((y.double() >= bf16(g - bound)) & (y.double() <= bf16(g + bound))).all()
