@@ -2,6 +2,8 @@
 // workgroup has, where an activation row lies, and the block product.
 #pragma once
 
+#include <algorithm>
+
 #include "rows_device.h"
 
 namespace moe {
@@ -20,13 +22,24 @@ struct GroupedArgs {
   int col_tiles;  // column tiles of an expert's output
 };
 
-// A workgroup's tile: expert e, grouped rows [row, end) of which it takes the
-// first ones, column tile `col`. e < 0: no tile is left for it.
+enum Epilogue { kOutBf16, kOutSwiglu };
+
+// Read-only data at addresses that are the same for the whole wave, through
+// the scalar cache (loads that the vector memory counter does not wait for).
+typedef const __attribute__((address_space(4))) float* uniform_floats;
+__device__ __forceinline__ uniform_floats as_uniform(const float* p) { return (uniform_floats)(uintptr_t)p; }
+
+// grouped_tile.hip
+void launch_grouped_tile(Epilogue epi, bool mx, GroupedArgs a, hipStream_t stream);
+
+// A workgroup's tile: grouped rows [row, end) of expert e, column tile `col`.
+// e < 0: no tile is left for it.
 struct TileAt {
   int e, row, end, col;
 };
 
-// The workgroup's tile when every expert's rows are cut into tiles of kRows.
+// The workgroup's tile when every expert's rows are cut into as few tiles of
+// at most kRows (a multiple of 16) as can be, even but for 16 rows.
 // The row tiles are counted anew by every workgroup (offsets are on the
 // device; E + 1 of them from L2 and one sum over the workgroup, about 1 us).
 // Tiles are numbered expert by expert, inside an expert column tile by column
@@ -80,8 +93,11 @@ __device__ __forceinline__ TileAt find_tile(const GroupedArgs& a, int block) {
       if (t >= before && t < before + tiles[q]) {
         const int mine = (int)(at - (int64_t)before * a.col_tiles);
         found[0] = tid * per + q;
-        found[1] = lo[q] + (mine % tiles[q]) * kRows;
-        found[2] = clamped(tid * per + q + 1);
+        // the expert's 16-row groups, evenly over its tiles
+        const int end = clamped(tid * per + q + 1), i = mine % tiles[q];
+        const int groups = (end - lo[q] + 15) / 16;
+        found[1] = lo[q] + 16 * (int)((int64_t)groups * i / tiles[q]);
+        found[2] = min(lo[q] + 16 * (int)((int64_t)groups * (i + 1) / tiles[q]), end);
         found[3] = mine / tiles[q];
       }
       before += tiles[q];
@@ -136,20 +152,16 @@ __device__ __forceinline__ float4_t product_f16(const Wide& w, const Wide& x) {
   return p;
 }
 
-// Scales of a lane's two halves under MXFP8, from its row's four E8M0 bytes
-// of a block (32 positions each): the largest byte as the block's own scale,
-// the others relative to it, which keeps every product inside F16 (an element
+// MXFP8 scales from a row's four E8M0 bytes of a block (32 positions each): the
+// largest as the block's own scale, the four relative to it, which keeps every product inside F16 (an element
 // 2^15 and more below the largest block's loses bits that lie below an FP32
 // sum's).
-struct MxScales {
-  float lo, hi, block;
-};
-__device__ __forceinline__ MxScales mx_scales(uint32_t bytes, int g) {
+__device__ __forceinline__ float mx_scales(uint32_t bytes, float (&rel)[4]) {
   const auto byte = [&](int b) { return (int)((bytes >> (8 * b)) & 0xFFu); };
   const int top = max(max(byte(0), byte(1)), max(byte(2), byte(3)));
-  const auto rel = [&](int b) { return __uint_as_float((uint32_t)max(127 + byte(b) - top, 1) << 23); };
-  const bool odd = g >= 2;  // bytes 16g .. 16g+15 lie in block g / 2, 64 further in block 2 + g / 2
-  return MxScales{rel(odd ? 1 : 0), rel(odd ? 3 : 2), __uint_as_float(top ? (uint32_t)top << 23 : 0x400000u)};
+#pragma unroll
+  for (int b = 0; b < 4; ++b) rel[b] = __uint_as_float((uint32_t)max(127 + byte(b) - top, 1) << 23);
+  return __uint_as_float(top ? (uint32_t)top << 23 : 0x400000u);
 }
 
 // gate / (1 + exp(-gate)) * up with both clamped. A clamped NaN stays one.

@@ -10,8 +10,6 @@
 namespace moe {
 namespace {
 
-enum Epilogue { kOutBf16, kOutSwiglu };
-
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 
@@ -54,8 +52,8 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_stream_kernel(GroupedArgs
     const int n = n0 + (m / 4) * kWide + t * 4 + (m & 3) + gate * I;
     wp[s] = a.w + ((size_t)at.e * a.N + n) * a.K + g * 16;
   }
-  const float* sw0 = a.ws + ((size_t)at.e * (a.N / 128) + n0 / 128) * KB;
-  const float* sw1 = kGlu ? sw0 + (size_t)(I / 128) * KB : sw0;
+  const uniform_floats sw0 = as_uniform(a.ws) + ((size_t)at.e * (a.N / 128) + n0 / 128) * KB;
+  const uniform_floats sw1 = kGlu ? sw0 + (size_t)(I / 128) * KB : sw0;
 
   const uint8_t* xp[kJ];
   const uint8_t* xsp[kJ];
@@ -104,9 +102,9 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_stream_kernel(GroupedArgs
         for (int j = 0; j < kJ; ++j) {
           if (j < subs) {
             if (kMx) {
-              const MxScales ms = mx_scales(xsr[d][j], g);
-              xs[j] = ms.block;
-              xw[j] = widen(xr[d][j][0], xr[d][j][1], ms.lo, ms.hi);
+              float rel[4];  // bytes 16g .. 16g+15 lie in block g / 2, 64 further in block 2 + g / 2
+              xs[j] = mx_scales(xsr[d][j], rel);
+              xw[j] = widen(xr[d][j][0], xr[d][j][1], g < 2 ? rel[0] : rel[1], g < 2 ? rel[2] : rel[3]);
             } else {
               xs[j] = __uint_as_float(xsr[d][j]);
               xw[j] = widen(xr[d][j][0], xr[d][j][1]);
@@ -199,10 +197,12 @@ void launch_stream(GroupedArgs a, hipStream_t stream) {
                      dim3(kThreads), 0, stream, a);
 }
 
-template <int kEpi, bool kMx>
+template <Epilogue kEpi, bool kMx>
 void launch(const GroupedArgs& a, hipStream_t stream) {
   if ((int64_t)a.R <= (int64_t)a.E * 8)
     launch_stream<kEpi, kMx, 1, 4, 4>(a, stream);
+  else if ((int64_t)a.R > (int64_t)a.E * 32)
+    launch_grouped_tile(kEpi, kMx, a, stream);
   else
     launch_stream<kEpi, kMx, 2, 4, 2>(a, stream);
 }
