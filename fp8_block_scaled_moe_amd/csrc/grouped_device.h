@@ -39,7 +39,7 @@ struct TileAt {
 };
 
 // The workgroup's tile when every expert's rows are cut into as few tiles of
-// at most kRows (a multiple of 16) as can be, even but for 16 rows.
+// at most kRows (a multiple of kGroup) as can be, even but for kGroup rows.
 // The row tiles are counted anew by every workgroup (offsets are on the
 // device; E + 1 of them from L2 and one sum over the workgroup, about 1 us).
 // Tiles are numbered expert by expert, inside an expert column tile by column
@@ -47,7 +47,7 @@ struct TileAt {
 // each XCD (workgroup id mod 8) takes a contiguous eighth of the numbers, so
 // that what neighbours share meets in one L2. Every thread calls it; barriers
 // inside.
-template <int kRows, int kThreadsWg>
+template <int kRows, int kGroup, int kThreadsWg>
 __device__ __forceinline__ TileAt find_tile(const GroupedArgs& a, int block) {
   constexpr int kWavesWg = kThreadsWg / kWave;
   constexpr int kPer = 1024 / kThreadsWg;  // experts per thread: E <= 1024
@@ -93,11 +93,11 @@ __device__ __forceinline__ TileAt find_tile(const GroupedArgs& a, int block) {
       if (t >= before && t < before + tiles[q]) {
         const int mine = (int)(at - (int64_t)before * a.col_tiles);
         found[0] = tid * per + q;
-        // the expert's 16-row groups, evenly over its tiles
+        // the expert's groups of kGroup rows, evenly over its tiles
         const int end = clamped(tid * per + q + 1), i = mine % tiles[q];
-        const int groups = (end - lo[q] + 15) / 16;
-        found[1] = lo[q] + 16 * (int)((int64_t)groups * i / tiles[q]);
-        found[2] = min(lo[q] + 16 * (int)((int64_t)groups * (i + 1) / tiles[q]), end);
+        const int groups = (end - lo[q] + kGroup - 1) / kGroup;
+        found[1] = lo[q] + kGroup * (int)((int64_t)groups * i / tiles[q]);
+        found[2] = min(lo[q] + kGroup * (int)((int64_t)groups * (i + 1) / tiles[q]), end);
         found[3] = mine / tiles[q];
       }
       before += tiles[q];
@@ -118,10 +118,6 @@ __device__ __forceinline__ int x_row(const GroupedArgs& a, int i) {
   return r >= 0 && r < a.X ? r : -1;
 }
 
-// Lane l = 16 g + r of a 128-wide K block holds bytes 16g .. 16g+15 (lo) and
-// 64+16g .. 64+16g+15 (hi) of row r: the register layout of the 16x16x128 FP8
-// instruction, used for weights and activations alike.
-
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
 // Eight e4m3 codes as F16 values times a power of two.
@@ -131,25 +127,6 @@ __device__ __forceinline__ half8_t widen8_scaled(uint32_t w0, uint32_t w1, float
   const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, scale, false);
   const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, scale, true);
   return half8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-}
-
-// A lane's 32 codes of a block as F16: exact, or times a power of two for
-// each half.
-struct Wide {
-  half8_t v[4];
-};
-__device__ __forceinline__ Wide widen(const u32x4_t& lo, const u32x4_t& hi, float slo = 1.f, float shi = 1.f) {
-  return Wide{{widen8_scaled(lo[0], lo[1], slo), widen8_scaled(lo[2], lo[3], slo), widen8_scaled(hi[0], hi[1], shi),
-               widen8_scaled(hi[2], hi[3], shi)}};
-}
-
-// The 16 x 16 products of a block, exact F16 products summed in FP32: lane
-// 16 g + r gets activation row r by weight rows 4g .. 4g+3.
-__device__ __forceinline__ float4_t product_f16(const Wide& w, const Wide& x) {
-  float4_t p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.v[i], x.v[i], p, 0, 0, 0);
-  return p;
 }
 
 // MXFP8 scales from a row's four E8M0 bytes of a block (32 positions each): the

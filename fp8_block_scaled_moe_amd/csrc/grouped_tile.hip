@@ -1,5 +1,5 @@
-// Products grouped by expert, many rows per expert (see grouped_gemm.hip for
-// few): 128 x 256 tiles through LDS and the F16 matrix instructions.
+// Products grouped by expert: tiles of up to 128 rows by 256 weight rows through
+// LDS and the F16 matrix instructions.
 #include <hip/hip_runtime.h>
 
 #include "grouped_device.h"
@@ -45,25 +45,17 @@ struct Shared {
 
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
-// A lane's 64 bytes of one block of a 32-row operand in F16: lane 32 h + r
-// has bytes 16 (h + 2 c) .. + 15 of row r for c = 0..3, two instructions' worth
-// each.
-struct Wide64 {
-  half8_t v[8];
+// Sixteen codes of a row in F16, two instructions' worth.
+struct Wide16 {
+  half8_t v[2];
 };
-__device__ __forceinline__ Wide64 read_wide(const uint8_t* p, const int (&off)[4], const float (&scale)[4]) {
-  Wide64 r;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const u32x4_t q = *reinterpret_cast<const u32x4_t*>(p + off[c]);
-    r.v[2 * c] = widen8_scaled(q[0], q[1], scale[c]);
-    r.v[2 * c + 1] = widen8_scaled(q[2], q[3], scale[c]);
-  }
-  return r;
+__device__ __forceinline__ Wide16 widen16(const u32x4_t& q, float scale) {
+  return Wide16{{widen8_scaled(q[0], q[1], scale), widen8_scaled(q[2], q[3], scale)}};
 }
 
 template <int kEpi, bool kMx, int kJ>
-__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared& sm) {
+__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared& sm, int first) {
+  constexpr int kN = kJ ? kJ : 1;
   constexpr bool kGlu = kEpi == kOutSwiglu;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -81,8 +73,8 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const uint8_t *xp[2], *wp[4];
   const int lr = lane >> 3;
   const auto chunk = [&](int L) { return ((lane & 7) ^ ((L >> 1) & 7)) * 16; };
-  const auto x_of = [&](int L) {  // activation row of LDS row L: kJ groups of 32 for each half of the waves
-    const int m = min(L & 63, 32 * kJ - 1) + (L >> 6) * 32 * kJ;
+  const auto x_of = [&](int L) {  // activation row of LDS row L
+    const int m = (L & 63) + (L >> 6) * 32 * first;
     return (size_t)max(x_row(a, min(at.row + m, last)), 0);
   };
 #pragma unroll
@@ -119,7 +111,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const uniform_floats sw0 = as_uniform(a.ws) + ((size_t)at.e * (a.N / 128) + min(n0, a.N - 1) / 128) * KB;
   const uniform_floats sw1 = kGlu ? sw0 + (size_t)(I / 128) * KB : sw0;
 
-  float16_t acc[kJ][2];
+  float16_t acc[kN][2];
 #pragma unroll
   for (int j = 0; j < kJ; ++j)
 #pragma unroll
@@ -130,57 +122,96 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   int off[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) off[c] = r32 * 128 + (((h + 2 * c) ^ (r32 >> 1)) & 7) * 16;
-  const float ones[4] = {1.f, 1.f, 1.f, 1.f};
 
-  issue(0, 0);
-  if (KB > 1) issue(1, 1);
-  int st = 0;
-  for (int kb = 0; kb < KB; ++kb) {
-    const float s0 = sw0[kb], s1 = kGlu ? sw1[kb] : s0;
-    if (kb + 1 < KB)
+  if (wm) __builtin_amdgcn_s_setprio(1);
+  // Sixteen bytes of every row (chunk h + 2 c of the lane's row) at a time,
+  // widened while the matrix instructions of the chunk before run; the scaled
+  // sums of a block are added while the next block's first ones run.
+  Wide16 w[2][2], x[2][kN];  // [chunk parity]
+  float rel[kN][4], sc[kN][2];
+  const auto scales = [&](int st, int kb, float (&xs)[kN]) {
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      const uint32_t sx = sm.st[st].xs[wm * 64 + j * 32 + r32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) rel[j][c] = 1.f;
+      xs[j] = kMx ? mx_scales(sx, rel[j]) : __uint_as_float(sx);
+    }
+  };
+  const auto load = [&](int st, int c) {
+    if (!kJ) return;
+    const uint8_t *wb = sm.st[st].w + wn * 64 * 128, *xb = sm.st[st].x + wm * 64 * 128;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) w[c & 1][t] = widen16(*reinterpret_cast<const u32x4_t*>(wb + t * 4096 + off[c]), 1.f);
+#pragma unroll
+    for (int j = 0; j < kJ; ++j)
+      x[c & 1][j] = widen16(*reinterpret_cast<const u32x4_t*>(xb + j * 4096 + off[c]), rel[j][c]);
+  };
+  float16_t p[kN][2];
+  const float16_t zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const auto add = [&](int j, int t) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[j][t][i] = fmaf(p[j][t][i], sc[j][t], acc[j][t][i]);
+  };
+  const auto multiply = [&](int c, bool first) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          p[j][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w[c & 1][t].v[i], x[c & 1][j].v[i],
+                                                           first && i == 0 ? zero : p[j][t], 0, 0, 0);
+        }
+  };
+  const auto ready = [&](bool more) {  // block kb's copies have ended, in every wave
+    if (more)
       copies_left<kCopies>(&sm);
     else
       copies_left<0>(&sm);
-    __builtin_amdgcn_s_barrier();  // every wave's copies of this block are there, and its reads of the block before are over
+    __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (kb + 2 < KB) issue(st == 0 ? 2 : st - 1, kb + 2);
-    const Stage& s = sm.st[st];
-    Wide64 w[2];
+  };
+
+  issue(0, 0);
+  if (KB > 1) issue(1, 1);
+  ready(KB > 1);
+  if (KB > 2) issue(2, 2);
+  float xs[kN];
+  scales(0, 0, xs);
+  load(0, 0);
+  int st = 0;
+  for (int kb = 0; kb < KB; ++kb) {
+    const float s0 = sw0[kb], s1 = kGlu ? sw1[kb] : s0;
+    load(st, 1);
+    multiply(0, true);
+    load(st, 2);
+    multiply(1, false);
+    load(st, 3);
+    multiply(2, false);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) w[t] = read_wide(s.w + (wn * 64 + t * 32) * 128, off, ones);
+    for (int j = 0; j < kJ; ++j)
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-      const uint32_t sx = s.xs[wm * 64 + j * 32 + r32];
-      float rel[4] = {1.f, 1.f, 1.f, 1.f}, xs;
-      if (kMx)
-        xs = mx_scales(sx, rel);
-      else
-        xs = __uint_as_float(sx);
-      const Wide64 x = read_wide(s.x + (wm * 64 + j * 32) * 128, off, rel);
-      float16_t p[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[t][i] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) p[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w[t].v[i], x.v[i], p[t], 0, 0, 0);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float sc = xs * (kGlu && t ? s1 : s0);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[j][t][i] = fmaf(p[t][i], sc, acc[j][t][i]);
-      }
+      for (int t = 0; t < 2; ++t) sc[j][t] = xs[j] * (t ? s1 : s0);
+    if (kb + 1 < KB) {
+      ready(kb + 2 < KB);  // and every wave has read all of block kb
+      if (kb + 3 < KB) issue(st, kb + 3);
+      st = st == 2 ? 0 : st + 1;
+      scales(st, kb + 1, xs);
+      load(st, 0);
     }
-    st = st == 2 ? 0 : st + 1;
+    multiply(3, false);
+#pragma unroll
+    for (int j = 0; j < kJ; ++j)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) add(j, t);
   }
 
   if (!kGlu) {
     if (n0 >= a.N) return;
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
-      const int i = at.row + (wm * kJ + j) * 32 + r32;
+      const int i = at.row + (wm * first + j) * 32 + r32;
       if (i <= last) {
         const bool none = x_row(a, i) < 0;
         uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)i * a.N + n0 + h * 16;
@@ -212,7 +243,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kJ; ++j) {
-    const int i = at.row + (wm * kJ + j) * 32 + r32;
+    const int i = at.row + (wm * first + j) * 32 + r32;
     if (i <= last) {
       float amax = kAmaxFloor;
 #pragma unroll
@@ -235,12 +266,19 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
 template <int kEpi, bool kMx>
 __global__ __launch_bounds__(kThreads, 2) void grouped_tile_kernel(GroupedArgs a) {
   __shared__ Shared sm;
-  const TileAt at = find_tile<kRows, kThreads>(a, blockIdx.x);
+  const TileAt at = find_tile<kRows, 32, kThreads>(a, blockIdx.x);
   if (at.e < 0) return;
-  if (at.end - at.row > 64)
-    tile<kEpi, kMx, 2>(a, at, sm);
+  // 32-row groups: the first half of the waves takes `first` of them, the
+  // second half the rest, so that each SIMD has a wave of both. All branches
+  // meet the same barriers.
+  const int groups = (at.end - at.row + 31) / 32, first = (groups + 1) / 2;
+  const int mine = threadIdx.x < kThreads / 2 ? first : groups - first;
+  if (mine == 2)
+    tile<kEpi, kMx, 2>(a, at, sm, first);
+  else if (mine == 1)
+    tile<kEpi, kMx, 1>(a, at, sm, first);
   else
-    tile<kEpi, kMx, 1>(a, at, sm);
+    tile<kEpi, kMx, 0>(a, at, sm, first);
 }
 
 template <int kEpi, bool kMx>
