@@ -22,15 +22,13 @@ struct GroupedArgs {
   int col_tiles;  // column tiles of an expert's output
 };
 
-enum Epilogue { kOutBf16, kOutSwiglu };
-
 // Read-only data at addresses that are the same for the whole wave, through
 // the scalar cache (loads that the vector memory counter does not wait for).
 typedef const __attribute__((address_space(4))) float* uniform_floats;
 __device__ __forceinline__ uniform_floats as_uniform(const float* p) { return (uniform_floats)(uintptr_t)p; }
 
-// grouped_tile.hip
-void launch_grouped_tile(Epilogue epi, bool mx, GroupedArgs a, hipStream_t stream);
+void launch_grouped_product(bool mx, GroupedArgs a, hipStream_t stream);  // grouped_product.hip
+void launch_grouped_swiglu(bool mx, GroupedArgs a, hipStream_t stream);   // grouped_swiglu.hip
 
 // A workgroup's tile: grouped rows [row, end) of expert e, column tile `col`.
 // e < 0: no tile is left for it.
@@ -118,6 +116,41 @@ __device__ __forceinline__ int x_row(const GroupedArgs& a, int i) {
   return r >= 0 && r < a.X ? r : -1;
 }
 
+// Copies from memory straight into LDS: lane l's 16 (or 4) bytes go to byte
+// 16 l (4 l) behind `to`, the same for the whole wave. In assembly, since the
+// compiler waits for its own form of them before every later read of LDS,
+// whichever buffer it reads; no register is written, and copies_left() waits
+// until at most n of the wave's are on their way (they end in order). A
+// workgroup barrier behind it makes all waves' copies visible.
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<const uint8_t*>(((uint64_t)uniform((uint32_t)(v >> 32)) << 32) | uniform((uint32_t)v));
+}
+__device__ __forceinline__ void copy16_to_lds(const uint8_t* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uniform(to)), "v"(from));
+}
+__device__ __forceinline__ void copy4_to_lds(const uint8_t* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform(to)), "v"(from));
+}
+// The same from a uniform address plus the lane's offset.
+__device__ __forceinline__ void copy16_to_lds(const uint8_t* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform(to)), "v"(offset),
+               "s"(uniform(base)));
+}
+// At most kLeft copies are left, and all reads of LDS have returned.
+template <int kLeft>
+__device__ __forceinline__ void copies_left(const void* lds) {
+  asm volatile("s_waitcnt vmcnt(%1) lgkmcnt(0)" ::"v"(lds), "n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void workgroup_barrier() {
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
 // Eight e4m3 codes as F16 values times a power of two.
@@ -130,9 +163,9 @@ __device__ __forceinline__ half8_t widen8_scaled(uint32_t w0, uint32_t w1, float
 }
 
 // MXFP8 scales from a row's four E8M0 bytes of a block (32 positions each): the
-// largest as the block's own scale, the four relative to it, which keeps every product inside F16 (an element
-// 2^15 and more below the largest block's loses bits that lie below an FP32
-// sum's).
+// largest as the block's own scale, the four relative to it, which keeps every
+// product inside F16 (an element of 32 positions whose scale is 2^15 and more
+// below the largest loses bits that lie below an FP32 sum's).
 __device__ __forceinline__ float mx_scales(uint32_t bytes, float (&rel)[4]) {
   const auto byte = [&](int b) { return (int)((bytes >> (8 * b)) & 0xFFu); };
   const int top = max(max(byte(0), byte(1)), max(byte(2), byte(3)));

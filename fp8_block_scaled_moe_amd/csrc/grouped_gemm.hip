@@ -1,5 +1,6 @@
 // Products grouped by expert over ragged rows (include/moe_rows.h): the calls
-// moe_grouped_gemm and moe_grouped_swiglu, over grouped_tile.hip's kernel.
+// moe_grouped_gemm and moe_grouped_swiglu, over the kernels of
+// grouped_product.hip and grouped_swiglu.hip.
 #include <hip/hip_runtime.h>
 
 #include "../../include/moe_rows.h"
@@ -58,7 +59,7 @@ int moe_grouped_gemm(const moe_grouped_args* args, void* stream) {
   if (args->R == 0) return MOE_DECODE_OK;
   const GroupedArgs a = kernel_args(*args);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  launch_grouped_tile(kOutBf16, args->quant == MOE_QUANT_MXFP8, a, s);
+  launch_grouped_product(args->quant == MOE_QUANT_MXFP8, a, s);
   return hipGetLastError() == hipSuccess ? MOE_DECODE_OK : MOE_DECODE_ERR_HIP;
 }
 
@@ -71,7 +72,7 @@ int moe_grouped_swiglu(const moe_grouped_args* args, void* stream) {
   if (!args->out_scale || misaligned(args->out_scale, 4)) return MOE_DECODE_ERR_INVALID_ARG;
   const GroupedArgs a = kernel_args(*args);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  launch_grouped_tile(kOutSwiglu, args->quant == MOE_QUANT_MXFP8, a, s);
+  launch_grouped_swiglu(args->quant == MOE_QUANT_MXFP8, a, s);
   return hipGetLastError() == hipSuccess ? MOE_DECODE_OK : MOE_DECODE_ERR_HIP;
 }
 

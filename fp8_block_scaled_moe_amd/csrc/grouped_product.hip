@@ -1,0 +1,232 @@
+// moe_grouped_gemm: tiles of up to 256 rows by 256 weight rows through LDS and
+// the FP8 matrix instructions.
+#include <hip/hip_runtime.h>
+
+#include "grouped_device.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kGroup = 16;  // rows of a matrix instruction
+constexpr int kCols = 256;  // weight rows of a tile
+
+template <int kRows>
+struct Stage {
+  uint8_t x[kRows * 128];
+  uint8_t w[kCols * 128];
+  uint32_t xs[kRows];  // FP32 scales, or four E8M0 bytes
+};
+template <int kRows, int kStages>
+struct Shared {
+  Stage<kRows> st[kStages];  // K blocks: one read, the others on their way
+};
+
+__device__ __forceinline__ int8v_t read_operand(const uint8_t* p, int lo, int hi) {
+  const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p + lo), b = *reinterpret_cast<const u32x4_t*>(p + hi);
+  return int8v_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+
+// A 16 x 16 product of one block: lane 16 g + r gives bytes 16 g .. 16 g + 15
+// and 64 + 16 g .. of weight row r and of activation row r, and gets activation
+// row r by weight rows 4 g .. 4 g + 3. kMx: the instruction applies the
+// activations' E8M0 scales; lane 16 g + r gives that of positions 32 g .. of
+// row r.
+template <bool kMx>
+__device__ __forceinline__ float4_t product(const int8v_t& w, const int8v_t& x, int e8m0) {
+  const float4_t zero = {0.f, 0.f, 0.f, 0.f};
+  if (kMx) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, 0, 0, 0, 127, 0, e8m0);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, 0, 0, 0, 0, 0, 0);
+}
+
+// kJ: the most 16-row groups of a wave; `first`: those of the first four waves.
+template <bool kMx, int kRows, int kStages, int kJ>
+__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared<kRows, kStages>& sm, int groups) {
+  constexpr int kHalf = kRows / 2;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int wn = wave & 3, wm = wave >> 2;
+  const int KB = a.K / 128, first = (groups + 1) / 2;
+
+  // What this wave copies of a block: 32 LDS rows of the weights, kRows / 8 of
+  // the activations, 64 scales (the same ones by several waves, so that every
+  // wave has as many copies on its way). LDS row L keeps 16-byte chunk c of
+  // its row at place c ^ (L / 2 % 8), so that the 16 rows of a read phase
+  // differ in bank. A lane's results of the four instructions s of a block and
+  // group are 16 neighbouring columns: instruction s has weight rows r of
+  // columns 16 (r / 4) + 4 s + r % 4.
+  constexpr int kXCopies = kRows / 64, kCopies = 4 + kXCopies + 1;
+  const int lr = lane >> 3;
+  const auto x_of = [&](int L) {  // activation row of LDS row L
+    const int m = L % kHalf + L / kHalf * kGroup * first;
+    return (size_t)max(x_row(a, min(at.row + m, at.end - 1)), 0);
+  };
+  const uint8_t* xp[kXCopies];
+#pragma unroll
+  for (int i = 0; i < kXCopies; ++i) {
+    const int L = (wave * kXCopies + i) * 8 + lr;
+    xp[i] = a.x + x_of(L) * a.K + ((lane & 7) ^ ((L >> 1) & 7)) * 16;
+  }
+  // its weight rows: half of the columns of one wave's 64; eight i begins at
+  // column 32 (i % 2) + 4 (i / 2) and, where i is odd, at the other half's chunks
+  const int col = min(at.col * kCols + (wave >> 1) * 64, a.N - 64) + (wave & 1) * 8;
+  const uint8_t* wp = a.w + ((size_t)at.e * a.N + col) * a.K;
+  const uint32_t wrow = (uint32_t)((lr >> 2) * 16 + (lr & 3)) * (uint32_t)a.K, chunk = ((lane & 7) ^ (lr >> 1)) * 16;
+  const uint32_t woff[2] = {wrow + chunk, wrow + (chunk ^ 64)};
+  const int sl = wave % (kRows / 64) * 64;
+  const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + x_of(sl + lane) * KB * 4;
+  const uint32_t lds = lds_offset(&sm);
+  const auto issue = [&](int st, int kb) {
+    const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kRows>);
+    const size_t k0 = (size_t)kb * 128;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      copy16_to_lds(wp + k0 + (size_t)((i & 1) * 32 + (i >> 1) * 4) * a.K, woff[i & 1],
+                    to + (uint32_t)offsetof(Stage<kRows>, w) + (wave * 32 + i * 8) * 128);
+#pragma unroll
+    for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + k0, to + (wave * kXCopies + i) * 1024);
+    copy4_to_lds(sp + (size_t)kb * 4, to + (uint32_t)offsetof(Stage<kRows>, xs) + sl * 4);
+  };
+
+  const int n0 = at.col * kCols + wn * 64;
+  const uniform_floats sw = as_uniform(a.ws) + ((size_t)at.e * (a.N / 128) + min(n0, a.N - 1) / 128) * KB;
+  const int swz = (g ^ (r16 >> 1)) * 16;
+  const int w_lo = (wn * 64 + r16) * 128 + swz, x_lo = (wm * kHalf + r16) * 128 + swz;
+
+  float4_t acc[kJ][4];
+#pragma unroll
+  for (int j = 0; j < kJ; ++j)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) acc[j][s] = float4_t{0.f, 0.f, 0.f, 0.f};
+
+  // Block b's copies have ended, in every wave, and every wave has read all
+  // of the block before. The copies of kStages - 2 blocks behind may be on
+  // their way.
+  const auto ready = [&](int b) {
+    if (b + kStages - 2 < KB)
+      copies_left<(kStages - 2) * kCopies>(&sm);
+    else
+      copies_left<0>(&sm);
+    workgroup_barrier();
+  };
+#pragma unroll
+  for (int b = 0; b < kStages - 1; ++b)
+    if (b < KB) issue(b, b);
+  ready(0);
+  if (kStages - 1 < KB) issue(kStages - 1, kStages - 1);
+
+  int8v_t w[4], x[2];
+  uint32_t sx[2];
+  const auto load_w = [&](int st) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) w[s] = read_operand(sm.st[st].w + s * 2048, w_lo, w_lo ^ 64);
+  };
+  const auto load_x = [&](int st, int j) {
+    x[j & 1] = read_operand(sm.st[st].x + j * 2048, x_lo, x_lo ^ 64);
+    sx[j & 1] = sm.st[st].xs[wm * kHalf + j * 16 + r16];
+  };
+  float4_t p[2][4];
+  float sc[2];
+  const auto multiply = [&](int j, float s0) {
+    sc[j & 1] = kMx ? s0 : __uint_as_float(sx[j & 1]) * s0;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) p[j & 1][s] = product<kMx>(w[s], x[j & 1], (int)((sx[j & 1] >> (8 * g)) & 0xFFu));
+  };
+  const auto add = [&](int j) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][s][i] = fmaf(p[j & 1][s][i], sc[j & 1], acc[j][s][i]);
+      asm volatile("" : "+v"(acc[j][s]));  // here, not behind the loop's body, where every p would have to live until then
+    }
+  };
+  load_w(0);
+  load_x(0, 0);
+  int st = 0;
+  for (int b = 0; b < KB; ++b) {
+    const float s0 = sw[b];
+    // a group's scaled sums are added while the next group's instructions
+    // run; the fences keep the compiler from loading further ahead than the
+    // registers reach
+#pragma unroll
+    for (int j = 0; j + 1 < kJ; ++j) {
+      load_x(st, j + 1);
+      multiply(j, s0);
+      if (j) add(j - 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (b + 1 < KB) {
+      ready(b + 1);
+      if (b + kStages < KB) issue(st, b + kStages);
+    }
+    multiply(kJ - 1, s0);
+    if (kJ > 1) add(kJ - 2);
+    __builtin_amdgcn_sched_barrier(0);
+    st = st == kStages - 1 ? 0 : st + 1;
+    if (b + 1 < KB) {
+      load_w(st);
+      load_x(st, 0);
+    }
+    add(kJ - 1);
+  }
+
+  if (n0 >= a.N) return;
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) {
+    const int i = at.row + (wm * first + j) * kGroup + r16;
+    if (j < (wm ? groups - first : first) && i < at.end) {
+      const bool none = x_row(a, i) < 0;
+      uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)i * a.N + n0 + g * 16;
+#pragma unroll
+      for (int s = 0; s < 4; s += 2) {
+        const float4_t u = acc[j][s], v = acc[j][s + 1];
+        u32x4_t q = {bf16x2_bits(u[0], u[1]), bf16x2_bits(u[2], u[3]), bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])};
+        if (none) q = u32x4_t{0u, 0u, 0u, 0u};
+        *reinterpret_cast<u32x4_t*>(o + 4 * s) = q;
+      }
+    }
+  }
+}
+
+template <bool kMx, int kRows, int kStages>
+__global__ __launch_bounds__(kThreads, 2) void grouped_product_kernel(GroupedArgs a) {
+  __shared__ Shared<kRows, kStages> sm;
+  const TileAt at = find_tile<kRows, kGroup, kThreads>(a, blockIdx.x);
+  if (at.e < 0) return;
+  const int groups = (at.end - at.row + kGroup - 1) / kGroup;
+  const int need = (groups + 1) / 2;  // of the first half of the waves; the other half has the rest
+  if (kRows > 64) {
+    if (need > 6)
+      tile<kMx, kRows, kStages, kRows / 32>(a, at, sm, groups);
+    else if (need > 4)
+      tile<kMx, kRows, kStages, kRows / 32 < 6 ? kRows / 32 : 6>(a, at, sm, groups);
+    else if (need > 2)
+      tile<kMx, kRows, kStages, kRows / 32 < 4 ? kRows / 32 : 4>(a, at, sm, groups);
+    else
+      tile<kMx, kRows, kStages, 2>(a, at, sm, groups);
+  } else if (need > 1) {
+    tile<kMx, kRows, kStages, 2>(a, at, sm, groups);
+  } else {
+    tile<kMx, kRows, kStages, 1>(a, at, sm, groups);
+  }
+}
+
+template <bool kMx, int kRows, int kStages>
+void launch(const GroupedArgs& a, hipStream_t stream) {
+  const int64_t tiles = std::min<int64_t>(a.R, (int64_t)a.R / kRows + a.E) * a.col_tiles;
+  hipLaunchKernelGGL((grouped_product_kernel<kMx, kRows, kStages>), dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(kThreads), 0,
+                     stream, a);
+}
+
+}  // namespace
+
+void launch_grouped_product(bool mx, GroupedArgs a, hipStream_t stream) {
+  a.col_tiles = (a.N + kCols - 1) / kCols;
+  if ((int64_t)a.R <= (int64_t)a.E * 48)
+    mx ? launch<true, 64, 3>(a, stream) : launch<false, 64, 3>(a, stream);
+  else
+    mx ? launch<true, 256, 2>(a, stream) : launch<false, 256, 2>(a, stream);
+}
+
+}  // namespace moe
