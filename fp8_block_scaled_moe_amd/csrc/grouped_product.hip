@@ -77,15 +77,19 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const int sl = wave % (kRows / 64) * 64;
   const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + x_of(sl + lane) * KB * 4;
   const uint32_t lds = lds_offset(&sm);
-  const auto issue = [&](int st, int kb) {
+  constexpr int kWCopies = 4, kRest = kXCopies + 1;
+  const auto issue_w = [&](int st, int kb) {
     const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kRows>);
     const size_t k0 = (size_t)kb * 128;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kWCopies; ++i)
       copy16_to_lds(wp + k0 + (size_t)((i & 1) * 32 + (i >> 1) * 4) * a.K, woff[i & 1],
                     to + (uint32_t)offsetof(Stage<kRows>, w) + (wave * 32 + i * 8) * 128);
+  };
+  const auto issue_x = [&](int st, int kb) {
+    const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kRows>);
 #pragma unroll
-    for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + k0, to + (wave * kXCopies + i) * 1024);
+    for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + (size_t)kb * 128, to + (wave * kXCopies + i) * 1024);
     copy4_to_lds(sp + (size_t)kb * 4, to + (uint32_t)offsetof(Stage<kRows>, xs) + sl * 4);
   };
 
@@ -100,21 +104,20 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
 #pragma unroll
     for (int s = 0; s < 4; ++s) acc[j][s] = float4_t{0.f, 0.f, 0.f, 0.f};
 
-  // Block b's copies have ended, in every wave, and every wave has read all
-  // of the block before. The copies of kStages - 2 blocks behind may be on
-  // their way.
-  const auto ready = [&](int b) {
-    if (b + kStages - 2 < KB)
-      copies_left<(kStages - 2) * kCopies>(&sm);
-    else
-      copies_left<0>(&sm);
-    workgroup_barrier();
-  };
+  // The copies of blocks b .. b + kStages - 1 go on while block b is worked on:
+  // its weights are in registers from its beginning on, so their place is
+  // filled anew at once; its activations' place when they have all been read.
 #pragma unroll
-  for (int b = 0; b < kStages - 1; ++b)
-    if (b < KB) issue(b, b);
-  ready(0);
-  if (kStages - 1 < KB) issue(kStages - 1, kStages - 1);
+  for (int b = 0; b < kStages; ++b)
+    if (b < KB) {
+      issue_w(b, b);
+      issue_x(b, b);
+    }
+  if (kStages - 1 < KB)
+    copies_left<(kStages - 1) * kCopies>(&sm);
+  else
+    copies_left<0>(&sm);
+  workgroup_barrier();
 
   int8v_t w[4], x[2];
   uint32_t sx[2];
@@ -146,6 +149,11 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   int st = 0;
   for (int b = 0; b < KB; ++b) {
     const float s0 = sw[b];
+    if (b + kStages < KB) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      workgroup_barrier();  // every wave has read the block's weights
+      issue_w(st, b + kStages);
+    }
     // a group's scaled sums are added while the next group's instructions
     // run; the fences keep the compiler from loading further ahead than the
     // registers reach
@@ -157,8 +165,13 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
       __builtin_amdgcn_sched_barrier(0);
     }
     if (b + 1 < KB) {
-      ready(b + 1);
-      if (b + kStages < KB) issue(st, b + kStages);
+      // the next block is there, in every wave, and every wave has read all of this one
+      if (b + kStages < KB)
+        copies_left<(kStages - 2) * kCopies + kWCopies>(&sm);
+      else
+        copies_left<0>(&sm);
+      workgroup_barrier();
+      if (b + kStages < KB) issue_x(st, b + kStages);
     }
     multiply(kJ - 1, s0);
     if (kJ > 1) add(kJ - 2);
