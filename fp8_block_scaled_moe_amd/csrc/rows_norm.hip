@@ -18,6 +18,7 @@ namespace {
 constexpr int kVec = 8;        // columns per lane and chunk (16 bytes of BF16)
 constexpr int kBatch = 8;      // expert rows requested before they are added
 constexpr int kMaxPicks = 32;
+constexpr int kFewTokens = 512;
 
 __device__ __forceinline__ void unpack8(const u32x4_t& w, float (&v)[kVec]) {
 #pragma unroll
@@ -200,15 +201,17 @@ extern "C" int moe_add_rmsnorm_quant(const moe_norm_args* args, void* stream) {
       misaligned(a.residual_out, 16) || misaligned(a.out, 16) || misaligned(a.q, 16) || misaligned(a.pos, 4) ||
       misaligned(a.weights, 4) || (a.quant != MOE_QUANT_MXFP8 && misaligned(a.scale, 4)))
     return MOE_DECODE_ERR_INVALID_ARG;
-  const int lanes = a.D / kVec;  // one chunk each
+  // Lanes for one chunk each: many, with all of a row's loads on their way at
+  // once, for routed rows (whose positions come first) and for few tokens; a
+  // quarter of them, with more workgroups on a CU, for many plain rows.
+  const int lanes = a.D / kVec;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const auto waves = [](int n) { return (n + kWave - 1) / kWave * kWave; };
-  if (lanes <= 256)
+  const bool wide = routed || a.T <= kFewTokens;
+  if (lanes <= (wide ? 1024 : 256))
     launch_norm<1>(a, waves(lanes), s);
-  else if (lanes <= 512)
+  else if (wide || lanes <= 512)
     launch_norm<2>(a, waves((lanes + 1) / 2), s);
-  else if (lanes <= 1024)
-    launch_norm<4>(a, waves((lanes + 3) / 4), s);
   else
     launch_norm<4>(a, waves((lanes + 3) / 4), s);
   return hipGetLastError() == hipSuccess ? MOE_DECODE_OK : MOE_DECODE_ERR_HIP;
