@@ -106,8 +106,14 @@ def _where(dev, stream):
     return _here if stream is None and dev.index == torch.cuda.current_device() else _place(dev, stream)
 
 
+# The current stream's handle without an object around it, where this torch
+# has it (1.8 us less per call, of some 13).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(name, args, dev) -> None:
-    rc = getattr(lib(), name)(ctypes.byref(args), torch.cuda.current_stream(dev).cuda_stream)
+    rc = getattr(lib(), name)(ctypes.byref(args), _raw_stream(dev.index))
     if rc != OK:
         raise MoeDecodeError(rc, name)
 
@@ -164,13 +170,17 @@ def add_rmsnorm_quant(residual: Optional[torch.Tensor], gamma: Optional[torch.Te
     if not (want_residual or want_out or quant is not None):
         raise ValueError("no output is wanted")
     with _where(dev, stream):
-        new = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
-        res = (residual if inplace else new(T, D)) if want_residual else None
-        out = new(T, D) if want_out else None
+        if like.shape == (T, D):
+            new = lambda dtype: torch.empty_like(like, dtype=dtype)  # noqa: E731
+        else:
+            new = lambda dtype: like.new_empty((T, D), dtype=dtype)  # noqa: E731
+        res = (residual if inplace else new(torch.bfloat16)) if want_residual else None
+        out = new(torch.bfloat16) if want_out else None
         q = scale = None
         if quant is not None:
-            q = new(T, D, dtype=torch.uint8)
-            scale = new(T, D // 32, dtype=torch.uint8) if quant == "mxfp8" else new(T, D // 128, dtype=torch.float32)
+            q = new(torch.uint8)
+            scale = (like.new_empty((T, D // 32), dtype=torch.uint8) if quant == "mxfp8"
+                     else like.new_empty((T, D // 128), dtype=torch.float32))
         if T:
             _call("moe_add_rmsnorm_quant",
                   NormArgs(T, D, k, R, eps, QUANT[quant], rp, dp, yp, pp, wp, gp, None if res is None else res.data_ptr(),
@@ -195,10 +205,9 @@ def route_rows(logits: torch.Tensor, bias: torch.Tensor, *, top_k: int, routed_s
     if not (local_begin >= 0 and El >= 1 and local_begin + El <= E):
         raise ValueError(f"local experts [{local_begin}, {local_begin + El}) must lie in [0, {E})")
     with _where(dev, stream):
-        i32 = dict(dtype=torch.int32, device=dev)
-        ids, pos = torch.empty((T, top_k), **i32), torch.empty((T, top_k), **i32)
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-        offsets, rows = torch.empty(El + 1, **i32), torch.empty(T * top_k, **i32)
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        pos, weights = torch.empty_like(ids), torch.empty_like(ids, dtype=torch.float32)
+        offsets, rows = ids.new_empty(El + 1), ids.new_empty(T * top_k)
         need = lib().moe_route_rows_workspace(T, El)
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         _call("moe_route_rows",
