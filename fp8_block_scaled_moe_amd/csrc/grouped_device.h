@@ -22,6 +22,13 @@ struct GroupedArgs {
   int col_tiles;  // column tiles of an expert's output
 };
 
+// Workgroups that find_tile's tiles need at most (each expert's rows rounded
+// up, no tile without a row), a multiple of the XCDs.
+inline unsigned grouped_workgroups(const GroupedArgs& a, int rows) {
+  const int64_t tiles = std::min<int64_t>(a.R, (int64_t)a.R / rows + a.E) * a.col_tiles;
+  return (unsigned)((tiles + 7) / 8 * 8);
+}
+
 // Read-only data at addresses that are the same for the whole wave, through
 // the scalar cache (loads that the vector memory counter does not wait for).
 typedef const __attribute__((address_space(4))) float* uniform_floats;

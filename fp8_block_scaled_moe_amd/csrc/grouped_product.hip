@@ -1,5 +1,30 @@
-// moe_grouped_gemm: tiles of up to 256 rows by 256 weight rows through LDS and
-// the FP8 matrix instructions.
+// moe_grouped_gemm: up to 256 (64) rows of an expert by 256 weight rows per
+// workgroup, on the FP8 matrix instructions.
+//
+// Every 128-wide K block of the tile's activations and weights is copied into
+// LDS, read from there by eight waves, up to 128 (32) rows by 64 weight rows
+// each, and multiplied by the 16x16x128 instruction, a block's product per
+// instruction; its FP32 sums are multiplied by the block's scales when they are
+// added. The instruction adds eight products at a time, each cut off 14 bits
+// below the power of two of the largest (measured one product at a time), and
+// these sums in FP32: 2^-16 of a result on average, a hundredth of what the
+// rounding of the rows to BF16 moves. It runs at three times the rate of the
+// F16 instruction, which needs its operands widened too (the same kernel on it:
+// 2.4 ms where this one takes 1.4, for 65,536 rows over 256 experts, N = 7168,
+// K = 2048).
+//
+// The weights of a block are in registers from its beginning on, so their
+// place in LDS is refilled at once and the activations' place when they have
+// been read; the two halves of the waves share the tile's 16-row groups evenly
+// and a SIMD has a wave of each.
+//
+// Bounds, measured on MI355X. Few rows: the weights' bytes (one token, 8 experts,
+// N = 7168, K = 2048: 19.5 us, 6.0 TB/s; 16 rows for each of 64 experts: 5.9).
+// Many: the copies into LDS, 64 KB for 17 MFLOP, beside the matrix cores: 1.6
+// PFLOP/s for 512 rows for each of 64 experts, 1.9 without the copies; an FP8
+// library product without block scales reaches 2.7. Tiles of 64 rows, with
+// three blocks in LDS instead of two: 6% faster up to 20 rows an expert, as
+// fast at 28, 9% slower at 80.
 #include <hip/hip_runtime.h>
 
 #include "grouped_device.h"
@@ -227,8 +252,7 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_product_kernel(GroupedArg
 
 template <bool kMx, int kRows, int kStages>
 void launch(const GroupedArgs& a, hipStream_t stream) {
-  const int64_t tiles = std::min<int64_t>(a.R, (int64_t)a.R / kRows + a.E) * a.col_tiles;
-  hipLaunchKernelGGL((grouped_product_kernel<kMx, kRows, kStages>), dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(kThreads), 0,
+  hipLaunchKernelGGL((grouped_product_kernel<kMx, kRows, kStages>), dim3(grouped_workgroups(a, kRows)), dim3(kThreads), 0,
                      stream, a);
 }
 
@@ -236,7 +260,7 @@ void launch(const GroupedArgs& a, hipStream_t stream) {
 
 void launch_grouped_product(bool mx, GroupedArgs a, hipStream_t stream) {
   a.col_tiles = (a.N + kCols - 1) / kCols;
-  if ((int64_t)a.R <= (int64_t)a.E * 48)
+  if ((int64_t)a.R <= (int64_t)a.E * 24)  // the mean rows of an expert: see above
     mx ? launch<true, 64, 3>(a, stream) : launch<false, 64, 3>(a, stream);
   else
     mx ? launch<true, 256, 2>(a, stream) : launch<false, 256, 2>(a, stream);

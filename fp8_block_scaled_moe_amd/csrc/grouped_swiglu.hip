@@ -1,5 +1,24 @@
-// moe_grouped_swiglu: tiles of up to 128 rows by 128 hidden columns (256 weight
-// rows) through LDS and the F16 matrix instructions.
+// moe_grouped_swiglu: up to 128 rows of an expert by 128 hidden columns (256
+// weight rows, up and gate) per workgroup.
+//
+// Every 128-wide K block of the tile's activations and weights is copied into
+// LDS (48 KB, three blocks at a time), read from there by eight waves, 64 rows
+// by 32 up and 32 gate columns each, widened to F16 (exact) and multiplied by
+// the 32x32x16 instruction; the block's FP32 sums are multiplied by its scales
+// when they are added. F16 and not the FP8 instruction, because the hidden's
+// codes and scales are decided from these sums: the FP8 instruction adds eight
+// products at a time cut off 14 bits below the largest (measured; 2^-16 of a
+// result on average), which moves an FP32 scale by 1e-5, ten times what FP32
+// sums do. The two halves of the waves share the tile's 32-row groups evenly,
+// a SIMD has one wave of each, and row tiles of an expert are alike in size.
+//
+// Bounds, measured on MI355X. Few rows: the weights' bytes (4 tokens x 8 of 256
+// experts, K = 7168, I = 2048: 138 us, 6.5 TB/s). Many: the matrix cores at the
+// clock that their power allows: 1.0 PFLOP/s for 4,096 rows for each of 8
+// experts (K = 7168), 1.23 without the copies, 1.3 in a loop of the same
+// instructions on registers; a BF16 library product reaches 1.22. Tiles of 32
+// rows with four blocks in LDS gained 1% below 5 rows an expert and lost 9%
+// at 12, so there is one size.
 #include <hip/hip_runtime.h>
 
 #include "grouped_device.h"
@@ -8,17 +27,18 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kGroup = 32;     // rows of a matrix instruction
+constexpr int kGroup = 32;  // rows of a matrix instruction
+constexpr int kRows = 128;
+constexpr int kHalf = kRows / 2;  // of the LDS rows: a half of the waves
+constexpr int kStages = 3;        // K blocks in LDS: one read, the others on their way
 
-template <int kRows>
 struct Stage {
   uint8_t x[kRows * 128];
   uint8_t w[256 * 128];
-  uint32_t xs[kRows < 64 ? 64 : kRows];  // FP32 scales, or four E8M0 bytes
+  uint32_t xs[kRows];  // FP32 scales, or four E8M0 bytes
 };
-template <int kRows, int kStages>
 struct Shared {
-  Stage<kRows> st[kStages];  // K blocks: one read, the others on their way
+  Stage st[kStages];
   float amax[4][kRows];
 };
 
@@ -33,9 +53,9 @@ __device__ __forceinline__ Wide16 widen16(const u32x4_t& q, float scale) {
 }
 
 // kJ: the 32-row groups of this wave; `first`: those of the first four waves.
-template <bool kMx, int kRows, int kStages, int kJ>
-__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared<kRows, kStages>& sm, int first) {
-  constexpr int kN = kJ ? kJ : 1, kHalf = kRows < 64 ? 32 : kRows / 2;
+template <bool kMx, int kJ>
+__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared& sm, int first) {
+  constexpr int kN = kJ ? kJ : 1;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r32 = lane & 31, h = lane >> 5;
@@ -43,23 +63,22 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const int KB = a.K / 128, I = a.N / 2;
 
   // What this wave copies of a block: 32 LDS rows of the weights, 16 of the
-  // activations and 64 scales (fewer where a tile has fewer rows: then several
-  // waves copy the same, so that every wave has as many copies on its way).
-  // LDS row L keeps 16-byte chunk c of its row at place c ^ (L / 2 % 8), so
-  // that the 16 rows of a read phase differ in bank. A wave's results of an
-  // instruction are weight rows 8 a + 4 h + b (a, b = 0..3) of its 32: these
-  // are columns 16 h + 4 a + b, so that a lane's 16 are neighbours.
-  constexpr int kXCopies = kRows / 64 ? kRows / 64 : 1, kCopies = 4 + kXCopies + 1;
+  // activations and 64 scales (the same ones by four waves each, so that every
+  // wave has as many copies on its way). LDS row L keeps 16-byte chunk c of its
+  // row at place c ^ (L / 2 % 8), so that the 16 rows of a read phase differ in
+  // bank. A wave's results of an instruction are weight rows 8 a + 4 h + b (a,
+  // b = 0..3) of its 32: these are columns 16 h + 4 a + b, so that a lane's 16
+  // are neighbours.
+  constexpr int kXCopies = 2, kCopies = 4 + kXCopies + 1;
   const int lr = lane >> 3;
   const auto x_of = [&](int L) {  // activation row of LDS row L
     const int m = L % kHalf + L / kHalf * kGroup * first;
     return (size_t)max(x_row(a, min(at.row + m, at.end - 1)), 0);
   };
-  const int xl = kXCopies > 1 ? wave * 8 * kXCopies : (wave & (kRows / 8 - 1)) * 8;  // its first LDS row of the activations
   const uint8_t* xp[kXCopies];
 #pragma unroll
   for (int i = 0; i < kXCopies; ++i) {
-    const int L = xl + i * 8 + lr;
+    const int L = wave * 16 + i * 8 + lr;
     xp[i] = a.x + x_of(L) * a.K + ((lane & 7) ^ ((L >> 1) & 7)) * 16;
   }
   // up rows for even waves, the same columns' gate rows for odd ones; its
@@ -68,19 +87,19 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const uint8_t* wp = a.w + ((size_t)at.e * a.N + at.col * 128 + (wave >> 1) * 32 + (wave & 1) * I) * a.K;
   const uint32_t wrow = (uint32_t)((lr >> 2) * 16 + (lr & 3)) * (uint32_t)a.K, chunk = ((lane & 7) ^ (lr >> 1)) * 16;
   const uint32_t woff[2] = {wrow + chunk, wrow + (chunk ^ 64)};
-  const int sl = kRows < 64 ? 0 : wave % (kRows / 64) * 64;  // its first scale
-  const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + x_of(min(sl + lane, kRows - 1)) * KB * 4;
+  const int sl = (wave & 1) * 64;  // its first scale
+  const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + x_of(sl + lane) * KB * 4;
   const uint32_t lds = lds_offset(&sm);
   const auto issue = [&](int st, int kb) {
-    const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kRows>);
+    const uint32_t to = lds + st * (uint32_t)sizeof(Stage);
     const size_t k0 = (size_t)kb * 128;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       copy16_to_lds(wp + k0 + (size_t)(4 * i) * a.K, woff[i & 1],
-                    to + (uint32_t)offsetof(Stage<kRows>, w) + (wave * 32 + i * 8) * 128);
+                    to + (uint32_t)offsetof(Stage, w) + (wave * 32 + i * 8) * 128);
 #pragma unroll
-    for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + k0, to + (xl + i * 8) * 128);
-    copy4_to_lds(sp + (size_t)kb * 4, to + (uint32_t)offsetof(Stage<kRows>, xs) + sl * 4);
+    for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + k0, to + (wave * 16 + i * 8) * 128);
+    copy4_to_lds(sp + (size_t)kb * 4, to + (uint32_t)offsetof(Stage, xs) + sl * 4);
   };
 
   const uniform_floats su = as_uniform(a.ws) + ((size_t)at.e * (a.N / 128) + at.col) * KB;
@@ -212,39 +231,32 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   }
 }
 
-template <bool kMx, int kRows, int kStages>
+template <bool kMx>
 __global__ __launch_bounds__(kThreads, 2) void grouped_swiglu_kernel(GroupedArgs a) {
-  __shared__ Shared<kRows, kStages> sm;
+  __shared__ Shared sm;
   const TileAt at = find_tile<kRows, kGroup, kThreads>(a, blockIdx.x);
   if (at.e < 0) return;
-  // 32-row groups: the first half of the waves takes `first` of them, the
-  // second half the rest, so that each SIMD has a wave of both. All branches
-  // meet the same barriers.
+  // the first half of the waves takes `first` of the 32-row groups, the other
+  // the rest; all branches meet the same barriers
   const int groups = (at.end - at.row + kGroup - 1) / kGroup, first = (groups + 1) / 2;
   const int mine = threadIdx.x < kThreads / 2 ? first : groups - first;
-  if (kRows > 64 && mine == 2)
-    tile<kMx, kRows, kStages, kRows / 64 ? kRows / 64 : 1>(a, at, sm, first);
+  if (mine == 2)
+    tile<kMx, 2>(a, at, sm, first);
   else if (mine == 1)
-    tile<kMx, kRows, kStages, 1>(a, at, sm, first);
+    tile<kMx, 1>(a, at, sm, first);
   else
-    tile<kMx, kRows, kStages, 0>(a, at, sm, first);
-}
-
-template <bool kMx, int kRows, int kStages>
-void launch(const GroupedArgs& a, hipStream_t stream) {
-  const int64_t tiles = std::min<int64_t>(a.R, (int64_t)a.R / kRows + a.E) * a.col_tiles;
-  hipLaunchKernelGGL((grouped_swiglu_kernel<kMx, kRows, kStages>), dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(kThreads), 0,
-                     stream, a);
+    tile<kMx, 0>(a, at, sm, first);
 }
 
 }  // namespace
 
 void launch_grouped_swiglu(bool mx, GroupedArgs a, hipStream_t stream) {
   a.col_tiles = a.N / 256;
-  if ((int64_t)a.R <= (int64_t)a.E * 24)
-    mx ? launch<true, 32, 4>(a, stream) : launch<false, 32, 4>(a, stream);
+  const dim3 grid(grouped_workgroups(a, kRows));
+  if (mx)
+    hipLaunchKernelGGL(grouped_swiglu_kernel<true>, grid, dim3(kThreads), 0, stream, a);
   else
-    mx ? launch<true, 128, 3>(a, stream) : launch<false, 128, 3>(a, stream);
+    hipLaunchKernelGGL(grouped_swiglu_kernel<false>, grid, dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace moe
