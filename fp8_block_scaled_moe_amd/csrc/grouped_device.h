@@ -2,8 +2,6 @@
 // workgroup has, where an activation row lies, and the block product.
 #pragma once
 
-#include <algorithm>
-
 #include "rows_device.h"
 
 namespace moe {
@@ -22,17 +20,19 @@ struct GroupedArgs {
   int col_tiles;  // column tiles of an expert's output
 };
 
-// Workgroups that find_tile's tiles need at most (each expert's rows rounded
-// up, no tile without a row), a multiple of the XCDs.
-inline unsigned grouped_workgroups(const GroupedArgs& a, int rows) {
-  const int64_t tiles = std::min<int64_t>(a.R, (int64_t)a.R / rows + a.E) * a.col_tiles;
+// Workgroups that find_tile's tiles need at most for R grouped rows (each
+// expert's rows rounded up, no tile without a row), a multiple of the XCDs.
+__host__ __device__ inline unsigned grouped_workgroups(const GroupedArgs& a, int R, int rows) {
+  const int64_t full = (int64_t)R / rows + a.E, tiles = (full < R ? full : R) * a.col_tiles;
   return (unsigned)((tiles + 7) / 8 * 8);
 }
 
 // Read-only data at addresses that are the same for the whole wave, through
 // the scalar cache (loads that the vector memory counter does not wait for).
 typedef const __attribute__((address_space(4))) float* uniform_floats;
+typedef const __attribute__((address_space(4))) int32_t* uniform_ints;
 __device__ __forceinline__ uniform_floats as_uniform(const float* p) { return (uniform_floats)(uintptr_t)p; }
+__device__ __forceinline__ uniform_ints as_uniform(const int32_t* p) { return (uniform_ints)(uintptr_t)p; }
 
 void launch_grouped_product(bool mx, GroupedArgs a, hipStream_t stream);  // grouped_product.hip
 void launch_grouped_swiglu(bool mx, GroupedArgs a, hipStream_t stream);   // grouped_swiglu.hip
@@ -59,6 +59,10 @@ __device__ __forceinline__ TileAt find_tile(const GroupedArgs& a, int block) {
   static_assert(kPer >= 1, "every expert has a thread");
   __shared__ int wave_sum[kWavesWg];
   __shared__ int found[4];
+  // R may be far more than the rows that are there (one GPU's share of the
+  // experts): workgroups that these cannot need leave at once
+  if ((unsigned)block >= grouped_workgroups(a, min(max(as_uniform(a.offsets)[a.E], 0), a.R), kRows))
+    return TileAt{-1, 0, 0, 0};
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int per = (a.E + kThreadsWg - 1) / kThreadsWg;
   const auto clamped = [&](int e) { return min(max(a.offsets[min(e, a.E)], 0), a.R); };
@@ -126,9 +130,10 @@ __device__ __forceinline__ int x_row(const GroupedArgs& a, int i) {
 // Copies from memory straight into LDS: lane l's 16 (or 4) bytes go to byte
 // 16 l (4 l) behind `to`, the same for the whole wave. In assembly, since the
 // compiler waits for its own form of them before every later read of LDS,
-// whichever buffer it reads; no register is written, and copies_left() waits
-// until at most n of the wave's are on their way (they end in order). A
-// workgroup barrier behind it makes all waves' copies visible.
+// whichever buffer it reads; no register is written but M0, which nothing else
+// uses on this target, and copies_left() waits until at most n of the wave's
+// are on their way (they end in order). A workgroup barrier behind it makes
+// all waves' copies visible.
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }

@@ -252,7 +252,7 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_product_kernel(GroupedArg
 
 template <bool kMx, int kRows, int kStages>
 void launch(const GroupedArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((grouped_product_kernel<kMx, kRows, kStages>), dim3(grouped_workgroups(a, kRows)), dim3(kThreads), 0,
+  hipLaunchKernelGGL((grouped_product_kernel<kMx, kRows, kStages>), dim3(grouped_workgroups(a, a.R, kRows)), dim3(kThreads), 0,
                      stream, a);
 }
 

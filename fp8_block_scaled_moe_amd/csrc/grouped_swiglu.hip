@@ -252,7 +252,7 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_swiglu_kernel(GroupedArgs
 
 void launch_grouped_swiglu(bool mx, GroupedArgs a, hipStream_t stream) {
   a.col_tiles = a.N / 256;
-  const dim3 grid(grouped_workgroups(a, kRows));
+  const dim3 grid(grouped_workgroups(a, a.R, kRows));
   if (mx)
     hipLaunchKernelGGL(grouped_swiglu_kernel<true>, grid, dim3(kThreads), 0, stream, a);
   else

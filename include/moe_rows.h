@@ -142,7 +142,7 @@ size_t moe_route_rows_workspace(int32_t T, int32_t local_experts);
  * once). Grouped row i, offsets[e] <= i < offsets[e + 1], belongs to expert e
  * and reads activation row r = rows ? rows[i] : i:
  *   g[i, n] = sum_b w_scale[e, n/128, b] * sum_{c in block b} w[e, n, c] * x[r, c] * x_scale
- * in FP32 (see the note on the matrix cores below).
+ * with FP32 sums.
  *   x        [X, K] e4m3 with x_scale [X, K/128] FP32 (MOE_QUANT_FP8 or
  *            MOE_QUANT_FP8_P2) or [X, K/32] E8M0 bytes (MOE_QUANT_MXFP8);
  *            no E8M0 byte 255
@@ -154,15 +154,19 @@ size_t moe_route_rows_workspace(int32_t T, int32_t local_experts);
  *            no access out of bounds
  *   w        [E, N, K] e4m3, w_scale [E, N/128, K/128] FP32
  *   R        rows of the output
- * moe_grouped_gemm: out [R, N] BF16 = g, rounded once.
+ * moe_grouped_gemm: out [R, N] BF16 = g, rounded once. The FP8 matrix
+ *   instruction it uses adds the products of eight neighbouring columns cut off
+ *   14 bits below the power of two of the largest, and these sums in FP32: off
+ *   by some 2^-16 of a row's typical value before the rounding to BF16 (2^-9).
  * moe_grouped_swiglu: w = W13, N = 2I rows (0..I-1 up, I..2I-1 gate):
  *   up = clamp(g[n], +-limit), gate = min(g[I + n], limit),
  *   act = gate / (1 + exp(-gate)) * up,
  *   out [R, I] e4m3 with out_scale [R, I/128] FP32: MOE_QUANT_FP8 of act.
  *   ("mega_moe" page, hidden_block). exp and the reciprocal are the
- *   hardware's (act within about (|gate| + 4) * 2^-23 of its value), and act is
- *   multiplied by the reciprocal of its scale, so a code next to a rounding
- *   border may differ from moe_decode_run's.
+ *   hardware's (act within about (|gate| + 4) * 2^-23 of its value), the
+ *   products are exact and their sums FP32 throughout, and act is multiplied
+ *   by the reciprocal of its scale, so a code next to a rounding border may
+ *   differ from moe_decode_run's.
  * K and N multiples of 128 (N of 256 for the SwiGLU), at most
  * MOE_ROWS_MAX_DIM; E <= 1024; X, R >= 0, at most 2^31 - 1 tiles of work
  * (R/16 + E rows of N/256 tiles). FP8 and output arrays 16-byte aligned, E8M0

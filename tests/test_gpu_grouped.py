@@ -234,6 +234,48 @@ def test_offsets_outside_are_clamped(counts):
 
 
 @pytest.mark.parametrize("counts", [[4, 2], [40, 30], [300, 200]], ids=["few", "some", "many"])
+def test_rows_before_the_first_stay(counts):
+    """Offsets that do not begin at 0: the rows before the first expert's are
+    no expert's."""
+    d = make(counts, 256, 256, 24, extra=0)
+    want = call_gemm(d)
+    full = d["offsets"].clone()
+    d["offsets"][0] = 3
+    y = call_gemm(d)
+    assert torch.equal(y[3:], want[3:])
+    d["offsets"][:] = full
+
+
+def test_offsets_in_disorder_stay_inside():
+    """Offsets that do not ascend give some rows or other, and leave those
+    from the last offset's clamp on and everything around the output alone."""
+    import ctypes
+    from fp8_block_scaled_moe_amd import _rows, lib
+
+    d = make([100] * 8, 256, 256, 25, extra=0)
+    d["offsets"][:] = torch.tensor([0, 700, 20, 5, -9, 300, 2**31 - 1, 90, 400], dtype=torch.int32)
+    R = d["x"].shape[0]
+    big = torch.full((R + 64, 256), 3.0, dtype=torch.bfloat16, device=DEV)
+    out = big[32:32 + R]
+    a = _rows.GroupedArgs(R, R, 8, 256, 256, 1, 0.0, d["x"].data_ptr(), d["x_scale"].data_ptr(), None, d["offsets"].data_ptr(),
+                          d["w"].data_ptr(), d["w_scale"].data_ptr(), out.data_ptr(), None)
+    assert lib().moe_grouped_gemm(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert (big[:32] == 3.0).all() and (big[32 + R:] == 3.0).all()
+
+
+def test_a_share_of_many_rows():
+    """Room for many more rows than there are (one GPU's share): the same
+    bits as with room for just these."""
+    d = make([70, 0, 200, 30], 512, 384, 26, gather=True, extra=0)
+    want, (wh, ws) = call_gemm(d), check_swiglu(d)
+    d["rows"] = torch.cat([d["rows"], torch.full((9000,), -3, dtype=torch.int32, device=DEV)])
+    assert torch.equal(call_gemm(d)[:300], want)
+    h, s = grouped_swiglu(d["x"], d["x_scale"], d["w"], d["w_scale"], d["offsets"], limit=LIMIT, rows=d["rows"])
+    assert torch.equal(h[:300], wh) and torch.equal(s[:300], ws)
+
+
+@pytest.mark.parametrize("counts", [[4, 2], [40, 30], [300, 200]], ids=["few", "some", "many"])
 def test_nan_stays_in_its_row(counts):
     """A NaN code in a row of x, or in another expert's weights, reaches only
     the rows that contain it."""

@@ -132,9 +132,10 @@ def test_rows_behind_the_last_stay(T=100):
     assert 0 < n < T * k and (rows[n:] == -7).all() and (rows[:n] >= 0).all()
 
 
-def test_long_prompt_against_plain_operations():
-    """16,385 tokens (257 chunks): sorted by stable library sorts."""
-    T, E, k = 16385, 256, 8
+@pytest.mark.parametrize("T,E,k", [(8192, 64, 4), (8193, 40, 3), (16385, 256, 8), (65537, 72, 2), (70001, 16, 1)])
+def test_long_prompts_against_plain_operations(T, E, k):
+    """Around the sizes where a chunk's tokens change: sorted by stable
+    library sorts."""
     logits, bias = make(T, E, 12)
     r = route_rows(logits, bias, top_k=k, routed_scale=2.5)
     key = (1.0 / (1.0 + torch.exp(-logits.double()))).float() + bias
