@@ -78,9 +78,10 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   // the activations, 64 scales (the same ones by several waves, so that every
   // wave has as many copies on its way). LDS row L keeps 16-byte chunk c of
   // its row at place c ^ (L / 2 % 8), so that the 16 rows of a read phase
-  // differ in bank. A lane's results of the four instructions s of a block and
-  // group are 16 neighbouring columns: instruction s has weight rows r of
-  // columns 16 (r / 4) + 4 s + r % 4.
+  // differ in bank. A lane's results of instructions s = 0, 1 (2, 3) of a
+  // block and group are eight neighbouring columns and those of a row's four
+  // lanes 32: instruction s has weight rows r of columns 32 (s / 2) +
+  // 8 (r / 4) + 4 (s % 2) + r % 4.
   constexpr int kXCopies = kRows / 64, kCopies = 4 + kXCopies + 1;
   const int lr = lane >> 3;
   const auto x_of = [&](int L) {  // activation row of LDS row L
@@ -93,11 +94,11 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
     const int L = (wave * kXCopies + i) * 8 + lr;
     xp[i] = a.x + x_of(L) * a.K + ((lane & 7) ^ ((L >> 1) & 7)) * 16;
   }
-  // its weight rows: half of the columns of one wave's 64; eight i begins at
-  // column 32 (i % 2) + 4 (i / 2) and, where i is odd, at the other half's chunks
-  const int col = min(at.col * kCols + (wave >> 1) * 64, a.N - 64) + (wave & 1) * 8;
+  // its weight rows: 32 of the 64 columns of one wave; eight i begins at column
+  // 16 (i % 2) + 4 (i / 2) and, where i is odd, at the other half's chunks
+  const int col = min(at.col * kCols + (wave >> 1) * 64, a.N - 64) + (wave & 1) * 32;
   const uint8_t* wp = a.w + ((size_t)at.e * a.N + col) * a.K;
-  const uint32_t wrow = (uint32_t)((lr >> 2) * 16 + (lr & 3)) * (uint32_t)a.K, chunk = ((lane & 7) ^ (lr >> 1)) * 16;
+  const uint32_t wrow = (uint32_t)((lr >> 2) * 8 + (lr & 3)) * (uint32_t)a.K, chunk = ((lane & 7) ^ (lr >> 1)) * 16;
   const uint32_t woff[2] = {wrow + chunk, wrow + (chunk ^ 64)};
   const int sl = wave % (kRows / 64) * 64;
   const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + x_of(sl + lane) * KB * 4;
@@ -108,7 +109,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
     const size_t k0 = (size_t)kb * 128;
 #pragma unroll
     for (int i = 0; i < kWCopies; ++i)
-      copy16_to_lds(wp + k0 + (size_t)((i & 1) * 32 + (i >> 1) * 4) * a.K, woff[i & 1],
+      copy16_to_lds(wp + k0 + (size_t)((i & 1) * 16 + (i >> 1) * 4) * a.K, woff[i & 1],
                     to + (uint32_t)offsetof(Stage<kRows>, w) + (wave * 32 + i * 8) * 128);
   };
   const auto issue_x = [&](int st, int kb) {
@@ -215,13 +216,13 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
     const int i = at.row + (wm * first + j) * kGroup + r16;
     if (j < (wm ? groups - first : first) && i < at.end) {
       const bool none = x_row(a, i) < 0;
-      uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)i * a.N + n0 + g * 16;
+      uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)i * a.N + n0 + g * 8;
 #pragma unroll
       for (int s = 0; s < 4; s += 2) {
         const float4_t u = acc[j][s], v = acc[j][s + 1];
         u32x4_t q = {bf16x2_bits(u[0], u[1]), bf16x2_bits(u[2], u[3]), bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])};
         if (none) q = u32x4_t{0u, 0u, 0u, 0u};
-        *reinterpret_cast<u32x4_t*>(o + 4 * s) = q;
+        *reinterpret_cast<u32x4_t*>(o + 16 * s) = q;
       }
     }
   }
