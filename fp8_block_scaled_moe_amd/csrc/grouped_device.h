@@ -148,12 +148,19 @@ __device__ __forceinline__ void copy16_to_lds(const uint8_t* from, uint32_t to) 
 __device__ __forceinline__ void copy4_to_lds(const uint8_t* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform(to)), "v"(from));
 }
-// The same from a uniform address plus the lane's offset, for data that is not
-// read again soon (weights: 16 rows for each of 64 experts of 4096 x 7168, 318
-// us without the hint and 288 with it; tiles that share weights lose nothing).
+// The same from a uniform address plus the lane's offset. kOnce: with the
+// non-temporal hint, for data that is read once (weights of one row tile: 16
+// rows for each of 64 experts of 4096 x 7168, 288 us with it and 318 without;
+// where row tiles share them, it costs: 65,536 rows over 256 such experts fetch
+// 13.8 GB with it and 9.6 without).
+template <bool kOnce>
 __device__ __forceinline__ void copy16_to_lds(const uint8_t* base, uint32_t offset, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(uniform(to)), "v"(offset),
-               "s"(uniform(base)));
+  if (kOnce)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(uniform(to)), "v"(offset),
+                 "s"(uniform(base)));
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform(to)), "v"(offset),
+                 "s"(uniform(base)));
 }
 // At most kLeft copies are left, and all reads of LDS have returned.
 template <int kLeft>

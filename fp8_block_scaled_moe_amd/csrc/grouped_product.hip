@@ -65,7 +65,7 @@ __device__ __forceinline__ float4_t product(const int8v_t& w, const int8v_t& x, 
 }
 
 // kJ: the most 16-row groups of a wave; `first`: those of the first four waves.
-template <bool kMx, int kRows, int kStages, int kJ>
+template <bool kMx, int kRows, int kStages, bool kOnce, int kJ>
 __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared<kRows, kStages>& sm, int groups) {
   constexpr int kHalf = kRows / 2;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -109,7 +109,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
     const size_t k0 = (size_t)kb * 128;
 #pragma unroll
     for (int i = 0; i < kWCopies; ++i)
-      copy16_to_lds(wp + k0 + (size_t)((i & 1) * 16 + (i >> 1) * 4) * a.K, woff[i & 1],
+      copy16_to_lds<kOnce>(wp + k0 + (size_t)((i & 1) * 16 + (i >> 1) * 4) * a.K, woff[i & 1],
                     to + (uint32_t)offsetof(Stage<kRows>, w) + (wave * 32 + i * 8) * 128);
   };
   const auto issue_x = [&](int st, int kb) {
@@ -228,7 +228,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   }
 }
 
-template <bool kMx, int kRows, int kStages>
+template <bool kMx, int kRows, int kStages, bool kOnce>
 __global__ __launch_bounds__(kThreads, 2) void grouped_product_kernel(GroupedArgs a) {
   __shared__ Shared<kRows, kStages> sm;
   const TileAt at = find_tile<kRows, kGroup, kThreads>(a, blockIdx.x);
@@ -237,23 +237,23 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_product_kernel(GroupedArg
   const int need = (groups + 1) / 2;  // of the first half of the waves; the other half has the rest
   if (kRows > 64) {
     if (need > 6)
-      tile<kMx, kRows, kStages, kRows / 32>(a, at, sm, groups);
+      tile<kMx, kRows, kStages, kOnce, kRows / 32>(a, at, sm, groups);
     else if (need > 4)
-      tile<kMx, kRows, kStages, kRows / 32 < 6 ? kRows / 32 : 6>(a, at, sm, groups);
+      tile<kMx, kRows, kStages, kOnce, kRows / 32 < 6 ? kRows / 32 : 6>(a, at, sm, groups);
     else if (need > 2)
-      tile<kMx, kRows, kStages, kRows / 32 < 4 ? kRows / 32 : 4>(a, at, sm, groups);
+      tile<kMx, kRows, kStages, kOnce, kRows / 32 < 4 ? kRows / 32 : 4>(a, at, sm, groups);
     else
-      tile<kMx, kRows, kStages, 2>(a, at, sm, groups);
+      tile<kMx, kRows, kStages, kOnce, 2>(a, at, sm, groups);
   } else if (need > 1) {
-    tile<kMx, kRows, kStages, 2>(a, at, sm, groups);
+    tile<kMx, kRows, kStages, kOnce, 2>(a, at, sm, groups);
   } else {
-    tile<kMx, kRows, kStages, 1>(a, at, sm, groups);
+    tile<kMx, kRows, kStages, kOnce, 1>(a, at, sm, groups);
   }
 }
 
-template <bool kMx, int kRows, int kStages>
+template <bool kMx, int kRows, int kStages, bool kOnce>
 void launch(const GroupedArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((grouped_product_kernel<kMx, kRows, kStages>), dim3(grouped_workgroups(a, a.R, kRows)), dim3(kThreads), 0,
+  hipLaunchKernelGGL((grouped_product_kernel<kMx, kRows, kStages, kOnce>), dim3(grouped_workgroups(a, a.R, kRows)), dim3(kThreads), 0,
                      stream, a);
 }
 
@@ -261,10 +261,13 @@ void launch(const GroupedArgs& a, hipStream_t stream) {
 
 void launch_grouped_product(bool mx, GroupedArgs a, hipStream_t stream) {
   a.col_tiles = (a.N + kCols - 1) / kCols;
-  if ((int64_t)a.R <= (int64_t)a.E * 24)  // the mean rows of an expert: see above
-    mx ? launch<true, 64, 3>(a, stream) : launch<false, 64, 3>(a, stream);
+  const int64_t R = a.R, E = a.E;
+  if (R <= E * 24)  // the mean rows of an expert: see above
+    mx ? launch<true, 64, 3, true>(a, stream) : launch<false, 64, 3, true>(a, stream);
+  else if (R <= E * 128)  // few experts have a second row tile (56 experts of 44 rows: 101 us with the hint, 104 without)
+    mx ? launch<true, 256, 2, true>(a, stream) : launch<false, 256, 2, true>(a, stream);
   else
-    mx ? launch<true, 256, 2>(a, stream) : launch<false, 256, 2>(a, stream);
+    mx ? launch<true, 256, 2, false>(a, stream) : launch<false, 256, 2, false>(a, stream);
 }
 
 }  // namespace moe

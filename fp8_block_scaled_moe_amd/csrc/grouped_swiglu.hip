@@ -53,7 +53,7 @@ __device__ __forceinline__ Wide16 widen16(const u32x4_t& q, float scale) {
 }
 
 // kJ: the 32-row groups of this wave; `first`: those of the first four waves.
-template <bool kMx, int kJ>
+template <bool kMx, bool kOnce, int kJ>
 __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared& sm, int first) {
   constexpr int kN = kJ ? kJ : 1;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -95,7 +95,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
     const size_t k0 = (size_t)kb * 128;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      copy16_to_lds(wp + k0 + (size_t)(4 * i) * a.K, woff[i & 1],
+      copy16_to_lds<kOnce>(wp + k0 + (size_t)(4 * i) * a.K, woff[i & 1],
                     to + (uint32_t)offsetof(Stage, w) + (wave * 32 + i * 8) * 128);
 #pragma unroll
     for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + k0, to + (wave * 16 + i * 8) * 128);
@@ -231,7 +231,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   }
 }
 
-template <bool kMx>
+template <bool kMx, bool kOnce>
 __global__ __launch_bounds__(kThreads, 2) void grouped_swiglu_kernel(GroupedArgs a) {
   __shared__ Shared sm;
   const TileAt at = find_tile<kRows, kGroup, kThreads>(a, blockIdx.x);
@@ -241,11 +241,11 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_swiglu_kernel(GroupedArgs
   const int groups = (at.end - at.row + kGroup - 1) / kGroup, first = (groups + 1) / 2;
   const int mine = threadIdx.x < kThreads / 2 ? first : groups - first;
   if (mine == 2)
-    tile<kMx, 2>(a, at, sm, first);
+    tile<kMx, kOnce, 2>(a, at, sm, first);
   else if (mine == 1)
-    tile<kMx, 1>(a, at, sm, first);
+    tile<kMx, kOnce, 1>(a, at, sm, first);
   else
-    tile<kMx, 0>(a, at, sm, first);
+    tile<kMx, kOnce, 0>(a, at, sm, first);
 }
 
 }  // namespace
@@ -253,10 +253,10 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_swiglu_kernel(GroupedArgs
 void launch_grouped_swiglu(bool mx, GroupedArgs a, hipStream_t stream) {
   a.col_tiles = a.N / 256;
   const dim3 grid(grouped_workgroups(a, a.R, kRows));
-  if (mx)
-    hipLaunchKernelGGL(grouped_swiglu_kernel<true>, grid, dim3(kThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL(grouped_swiglu_kernel<false>, grid, dim3(kThreads), 0, stream, a);
+  const bool once = (int64_t)a.R <= (int64_t)a.E * 64;  // few experts have a second row tile
+  const auto kernel = mx ? (once ? grouped_swiglu_kernel<true, true> : grouped_swiglu_kernel<true, false>)
+                         : (once ? grouped_swiglu_kernel<false, true> : grouped_swiglu_kernel<false, false>);
+  hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace moe
