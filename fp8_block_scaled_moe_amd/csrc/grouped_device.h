@@ -172,21 +172,20 @@ __device__ __forceinline__ void workgroup_barrier() {
   asm volatile("" ::: "memory");
 }
 
-typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
-// Eight e4m3 codes as F16 values times a power of two.
-__device__ __forceinline__ half8_t widen8_scaled(uint32_t w0, uint32_t w1, float scale) {
-  const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, scale, false);
-  const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, scale, true);
-  const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, scale, false);
-  const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, scale, true);
-  return half8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+// Eight e4m3 codes as BF16 values times a power of two: exact, down to 2^-117.
+__device__ __forceinline__ bf16x8_t widen8_scaled(uint32_t w0, uint32_t w1, float scale) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, false);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, true);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, false);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, true);
+  return bf16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
 // MXFP8 scales from a row's four E8M0 bytes of a block (32 positions each): the
-// largest as the block's own scale, the four relative to it, which keeps every
-// product inside F16 (an element of 32 positions whose scale is 2^15 and more
-// below the largest loses bits that lie below an FP32 sum's).
+// largest as the block's own scale, the four relative to it, so that no
+// product is larger than FP32's range allows while its result is not.
 __device__ __forceinline__ float mx_scales(uint32_t bytes, float (&rel)[4]) {
   const auto byte = [&](int b) { return (int)((bytes >> (8 * b)) & 0xFFu); };
   const int top = max(max(byte(0), byte(1)), max(byte(2), byte(3)));

@@ -24,8 +24,8 @@ int check(const moe_grouped_args* p) {
   if (misaligned(a.x, 16) || misaligned(a.w, 16) || misaligned(a.out, 16) || misaligned(a.w_scale, 4) ||
       misaligned(a.offsets, 4) || misaligned(a.rows, 4) || misaligned(a.x_scale, 4))
     return MOE_DECODE_ERR_INVALID_ARG;
-  // workgroups of any form of the kernels: a grid's limit
-  if (((int64_t)a.R / 16 + a.E) * ((a.N + 255) / 256) > INT32_MAX - 8) return MOE_DECODE_ERR_UNSUPPORTED;
+  // a grid's limit, 2^32 threads (64-row tiles come with R <= 24 E only, far below it)
+  if (((int64_t)a.R / 128 + a.E) * ((a.N + 255) / 256) > (int64_t)(UINT32_MAX / 512) - 8) return MOE_DECODE_ERR_UNSUPPORTED;
   return MOE_DECODE_OK;
 }
 

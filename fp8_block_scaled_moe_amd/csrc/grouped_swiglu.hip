@@ -3,13 +3,15 @@
 //
 // Every 128-wide K block of the tile's activations and weights is copied into
 // LDS (48 KB, three blocks at a time), read from there by eight waves, 64 rows
-// by 32 up and 32 gate columns each, widened to F16 (exact) and multiplied by
+// by 32 up and 32 gate columns each, widened to BF16 (exact) and multiplied by
 // the 32x32x16 instruction; the block's FP32 sums are multiplied by its scales
-// when they are added. F16 and not the FP8 instruction, because the hidden's
+// when they are added. BF16 and not the FP8 instruction, because the hidden's
 // codes and scales are decided from these sums: the FP8 instruction adds eight
 // products at a time cut off 14 bits below the largest (measured; 2^-16 of a
 // result on average), which moves an FP32 scale by 1e-5, ten times what FP32
-// sums do. The two halves of the waves share the tile's 32-row groups evenly,
+// sums do. F16 is as exact (24 bits below the largest, both) for FP32 scales, a
+// hundredth slower (4.61 and 4.56 ms for 65,536 rows over 256 experts, K = 7168,
+// I = 2048), and too narrow for MXFP8 scales that lie 2^15 and more apart. The two halves of the waves share the tile's 32-row groups evenly,
 // a SIMD has one wave of each, and row tiles of an expert are alike in size.
 //
 // Bounds, measured on MI355X. Few rows: the weights' bytes (4 tokens x 8 of 256
@@ -44,9 +46,9 @@ struct Shared {
 
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
-// Sixteen codes of a row in F16, two instructions' worth.
+// Sixteen codes of a row in BF16, two instructions' worth.
 struct Wide16 {
-  half8_t v[2];
+  bf16x8_t v[2];
 };
 __device__ __forceinline__ Wide16 widen16(const u32x4_t& q, float scale) {
   return Wide16{{widen8_scaled(q[0], q[1], scale), widen8_scaled(q[2], q[3], scale)}};
@@ -143,7 +145,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           p[j][t] =
-              __builtin_amdgcn_mfma_f32_32x32x16_f16(w[c & 1][t].v[i], x[c & 1][j].v[i], c || i ? p[j][t] : zero, 0, 0, 0);
+              __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[c & 1][t].v[i], x[c & 1][j].v[i], c || i ? p[j][t] : zero, 0, 0, 0);
   };
   // Block b's copies have ended, in every wave, and every wave has read all
   // of the block before. The copies of kStages - 2 blocks behind may be on

@@ -189,7 +189,8 @@ extern "C" int moe_add_rmsnorm_quant(const moe_norm_args* args, void* stream) {
   const moe_norm_args& a = *args;
   if (a.T == 0) return MOE_DECODE_OK;
   if (a.T < 0 || a.R < 0 || a.k < 0 || !(a.eps >= 0.f) || !(a.eps <= 3.4e38f)) return MOE_DECODE_ERR_INVALID_ARG;
-  if (a.quant < MOE_QUANT_NONE || a.quant > MOE_QUANT_MXFP8 || a.k > kMaxPicks) return MOE_DECODE_ERR_UNSUPPORTED;
+  if (a.quant < MOE_QUANT_NONE || a.quant > MOE_QUANT_MXFP8 || a.k > kMaxPicks || a.T > MOE_ROWS_MAX_TOKENS)
+    return MOE_DECODE_ERR_UNSUPPORTED;
   const int unit = a.quant == MOE_QUANT_NONE ? kVec : a.quant == MOE_QUANT_MXFP8 ? 32 : 128;
   if (a.D <= 0 || a.D % unit || a.D > MOE_ROWS_MAX_D) return MOE_DECODE_ERR_UNSUPPORTED;
   if (!a.residual && !a.delta && !a.y) return MOE_DECODE_ERR_INVALID_ARG;

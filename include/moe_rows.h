@@ -53,7 +53,7 @@ extern "C" {
 #define MOE_QUANT_MXFP8 3
 
 #define MOE_ROWS_MAX_D 16384         /* longest row of moe_add_rmsnorm_quant */
-#define MOE_ROWS_MAX_TOKENS 1048576  /* tokens of one moe_route_rows call */
+#define MOE_ROWS_MAX_TOKENS 1048576  /* tokens of one moe_add_rmsnorm_quant or moe_route_rows call */
 #define MOE_ROWS_MAX_DIM 131072      /* N and K of the grouped products */
 
 /* Passages: "kimi_k3 ... ep.comm" page, EpCombine and rms_rstd (sum of a
@@ -78,8 +78,8 @@ extern "C" {
  *                (by `quant`); both NULL with MOE_QUANT_NONE
  * No other overlap of outputs with inputs. BF16 and e4m3 arrays 16-byte
  * aligned, the others to their element. D a multiple of 128 (FP8), 32 (MXFP8)
- * or 8 (no quantisation) up to MOE_ROWS_MAX_D; 0 <= k <= 32; eps >= 0,
- * finite. At least one output and at least one of residual, delta, y.
+ * or 8 (no quantisation) up to MOE_ROWS_MAX_D; T <= MOE_ROWS_MAX_TOKENS;
+ * 0 <= k <= 32; eps >= 0, finite. At least one output and at least one of residual, delta, y.
  * T = 0 is a valid empty call. */
 typedef struct moe_norm_args {
   int32_t T, D, k, R;
@@ -168,8 +168,8 @@ size_t moe_route_rows_workspace(int32_t T, int32_t local_experts);
  *   by the reciprocal of its scale, so a code next to a rounding border may
  *   differ from moe_decode_run's.
  * K and N multiples of 128 (N of 256 for the SwiGLU), at most
- * MOE_ROWS_MAX_DIM; E <= 1024; X, R >= 0, at most 2^31 - 1 tiles of work
- * (R/16 + E rows of N/256 tiles). FP8 and output arrays 16-byte aligned, E8M0
+ * MOE_ROWS_MAX_DIM; E <= 1024; X, R >= 0, at most 2^23 - 9 tiles of work
+ * (floor(R/128) + E rows of ceil(N/256) tiles). FP8 and output arrays 16-byte aligned, E8M0
  * bytes 4-byte aligned, the others to their element. R = 0 is a valid empty
  * call. */
 typedef struct moe_grouped_args {

@@ -194,6 +194,26 @@ def test_e8m0_range():
     check_gemm(d, 2.0**-126)  # results below the smallest normal may be flushed
 
 
+@pytest.mark.parametrize("counts", [[3, 2], [40, 30], [300, 200]], ids=["few", "some", "many"])
+def test_e8m0_scales_far_apart(counts):
+    """A block's 32 positions with a scale 2^30 above their neighbours', whose
+    codes (then whose weights) are zero: the neighbours' products are all
+    there is, and no bit of them may be lost."""
+    d = make(counts, 256, 512, 27, "mxfp8")
+    gen = torch.Generator(device=DEV).manual_seed(28)
+    s = torch.randint(100, 105, d["x_scale"].shape, generator=gen, device=DEV)
+    s[:, 1::4] = 135
+    d["x_scale"] = s.to(torch.uint8)
+    d["w_scale"] *= 2.0**18
+    far = (torch.arange(512, device=DEV) // 32) % 4 == 1
+    for n in ("x", "w"):
+        full = d[n].clone()
+        d[n].view(torch.uint8)[..., far] = 0
+        check_gemm(d)
+        check_swiglu(d)
+        d[n] = full
+
+
 @pytest.mark.parametrize("counts", [[3, 1], [40, 30], [300, 200]], ids=["few", "some", "many"])
 def test_rows_behind_the_last_stay(counts):
     """Rows of the output from offsets[E] on are left as they were."""

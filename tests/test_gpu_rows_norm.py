@@ -154,6 +154,13 @@ def test_empty():
     assert res.shape == out.shape == q.shape == (0, 256) and s.shape == (0, 2)
 
 
+def test_most_tokens():
+    """The longest call there is, in the narrowest rows."""
+    x = torch.randn(1048576, 8, generator=torch.Generator(device=DEV).manual_seed(42), device=DEV).to(torch.bfloat16)
+    res, out, _, _ = add_rmsnorm_quant(x, None, EPS, quant=None)
+    assert torch.equal(res, x) and torch.equal(out, x)
+
+
 @pytest.mark.parametrize("quant", ["fp8", "mxfp8"])
 def test_nan_and_infinity(quant):
     """A NaN or infinite value spoils its row (through rstd) and no other;

@@ -95,6 +95,21 @@ def test_infinite_logits():
     assert torch.equal(r.ids, want)
 
 
+@pytest.mark.parametrize("mask", [float("-inf"), torch.finfo(torch.float32).min], ids=["infinity", "lowest"])
+@pytest.mark.parametrize("T", [40, 150])
+def test_masked_experts(T, mask):
+    """Experts switched off by their bias are not picked while k others are
+    there, and are picked in their order where not."""
+    logits, bias = make(T, 100, 41)
+    bias[3:60] = mask
+    r = check(logits, bias, 8)
+    assert not ((r.ids >= 3) & (r.ids < 60)).any()
+    bias[5:] = mask
+    check(logits, bias, 8)
+    bias[:] = mask
+    check(logits, bias, 8)
+
+
 @pytest.mark.parametrize("T", [40, 200])
 def test_nan_logits_give_valid_places(T):
     """Whatever a NaN is routed to, every place is a row of the batch."""

@@ -55,7 +55,7 @@ NORM = dict(T=2, D=256, k=0, R=0, eps=1e-5, quant=1, residual=P, gamma=P, residu
     (dict(T=0, D=-1), 0),                                   # an empty call, whatever the rest
     (dict(T=-1), INVALID), (dict(k=-1), INVALID), (dict(R=-1), INVALID),
     (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
-    (dict(quant=4), UNSUPPORTED), (dict(quant=-1), UNSUPPORTED),
+    (dict(quant=4), UNSUPPORTED), (dict(quant=-1), UNSUPPORTED), (dict(T=1048577), UNSUPPORTED),
     (dict(D=0), UNSUPPORTED), (dict(D=192), UNSUPPORTED), (dict(D=16384 + 128), UNSUPPORTED),
     (dict(D=48, quant=3), UNSUPPORTED), (dict(D=12, quant=0, q=None, scale=None), UNSUPPORTED),
     (dict(residual=None), INVALID),                         # nothing to add
@@ -112,6 +112,7 @@ GROUPED = dict(R=4, X=4, E=2, N=256, K=256, quant=1, limit=7.0, x=P, x_scale=P, 
     (dict(N=131072 + 256), UNSUPPORTED), (dict(K=131072 + 128), UNSUPPORTED),
     (dict(quant=0), UNSUPPORTED), (dict(quant=4), UNSUPPORTED),
     (dict(X=3), INVALID), (dict(X=0, rows=P), INVALID),
+    (dict(R=2**31 - 1, X=2**31 - 1), UNSUPPORTED), (dict(R=2**25, X=2**25, N=8192), UNSUPPORTED),
     (dict(x=None), INVALID), (dict(x_scale=None), INVALID), (dict(offsets=None), INVALID), (dict(w=None), INVALID),
     (dict(w_scale=None), INVALID), (dict(out=None), INVALID),
     (dict(x=P + 8), INVALID), (dict(w=P + 8), INVALID), (dict(out=P + 8), INVALID), (dict(rows=P + 2), INVALID),
