@@ -7,10 +7,12 @@
 // expert, a 64-bit mask of the tokens that picked it (LDS or-atomics: the
 // same mask in any order), and a route's place is
 //   offset of the expert + count of earlier chunks + tokens below in the mask.
-// Up to 64 tokens one workgroup does all of it (one launch). Beyond, three:
+// Up to 32 tokens one workgroup does all of it (one launch). Beyond, three:
 // picks and counts per (chunk, expert), the running sums over the chunks,
-// and the places. The bound is the FP64 sigmoid and the selection (VALU), not
-// memory: 16 MB of logits for 16,384 tokens x 256 experts.
+// and the places. The bound is instructions, not memory: 16,384 tokens x 256
+// experts are 16 MB of logits (4 us), but some 370 vector instructions a token,
+// 12 of the first launch's 18 us; the other two take 4.7 and 4.3 us. One token:
+// 4.5 us, all of it latency.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -21,18 +23,23 @@
 namespace moe {
 namespace {
 
-constexpr int kOneLaunch = 64;  // most tokens of the single workgroup
+// Most tokens of the single workgroup: 32 tokens x 256 experts take it 9.7 us,
+// 64 16.3, where the three launches take 11.9 (in a graph, from 33 tokens on).
+constexpr int kOneLaunch = 32;
+constexpr int kMaxChunk = 64;  // tokens of a workgroup: a mask's bits
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / kWave;
 constexpr int kScanExperts = 16;  // experts per workgroup of the chunk sums
 constexpr int kScanBatch = 4;     // counts requested before they are added
 constexpr int kScanParts = kRouteThreads / kScanExperts;
 
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+
 // A bound that at least k of the wave's values reach, at most the k-th
 // largest: the largest such value found bit by bit below the leading bits that
 // all values share, ended as soon as exactly k reach it.
 __device__ __forceinline__ uint32_t kth_bound(uint32_t v, int k) {
-  const uint32_t hi = wave_max_u32(v), d = hi ^ wave_min_u32(v);
+  const uint32_t hi = uniform(wave_max_u32(v)), d = hi ^ uniform(wave_min_u32(v));
   if (d == 0) return hi;
   int b = 31 - __builtin_clz(d), n_ge = -1;
   uint32_t T = b == 31 ? 0u : (hi & ~((2u << b) - 1u));
@@ -61,8 +68,10 @@ __device__ __forceinline__ uint32_t kth_bound(uint32_t v, int k) {
 // where a key is NaN or infinity, fewer than k are finite, or the candidates do not fit the wave (equal
 // scores of many experts): then every expert gets its exact key.
 //
-// Measured for 16,384 tokens x 256 experts, top-8: 22.7 us with the exact key
-// of every expert, 13.1 so; 4,095 x 896, top-16, BF16: 53.8 and 13.9.
+// Measured (route_pick_kernel): 16,384 tokens x 256 experts, top-8, 22.7 us with
+// the exact key of every expert and 18.2 so; 4,095 x 896, top-16, BF16, 25.4
+// and 15.8. Candidates gathered through LDS instead of lane permutations: 19.0
+// and 17.1.
 template <int kPer>
 __device__ __forceinline__ bool pick_candidates(const float (&z)[kPer], const float (&bias)[kPer], int E, int k, int lane,
                                                 int& id, float& s_mine, float& total) {
@@ -110,13 +119,14 @@ __device__ __forceinline__ bool pick_candidates(const float (&z)[kPer], const fl
     }
   }
   const float score = sigmoid_f32(cz);
-  const uint32_t mine = ordered_key(score + cb);
+  const uint32_t mine = lane < n ? ordered_key(score + cb) : 0u;
   int rank = 0;
+#pragma unroll 1  // unrolled, the compiler compares with all 64 lanes
   for (int q0 = 0; q0 < n; q0 += 8) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {  // past n: lanes up to 63, not counted
-      const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, min(q0 + q, kWave - 1));
-      rank += q0 + q < n && (other > mine || (other == mine && q0 + q < lane)) ? 1 : 0;
+    for (int q = 0; q < 8; ++q) {  // lanes past n: the key 0, below every candidate's
+      const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, q0 + q);
+      rank += other > mine || (other == mine && q0 + q < lane) ? 1 : 0;
     }
   }
   const int to = (lane < n && rank < k ? rank : kWave - 1) * 4;
@@ -134,9 +144,10 @@ __device__ __forceinline__ bool pick_candidates(const float (&z)[kPer], const fl
 }
 
 // Tokens per workgroup when there are many: one or two per wave while that
-// gives the CUs two workgroups each, more (a mask's bits at most) where the
-// counts of the chunks would grow large.
-__host__ __device__ __forceinline__ int chunk_tokens(int T) { return T <= 8192 ? 16 : T <= 65536 ? 32 : 64; }
+// gives the CUs two workgroups each (4,095 tokens x 896 experts: 25 us with 16,
+// 51 with 64), more (a mask's bits at most) where the counts of the chunks,
+// which are read and written twice, would grow large.
+__host__ __device__ __forceinline__ int chunk_tokens(int T) { return T <= 8192 ? 16 : T <= 65536 ? 32 : kMaxChunk; }
 
 // The workgroup's chunk of n tokens from t0 on, a token per wave at a time (the
 // next one's logits on their way): ids and weights written, the picks also to
@@ -246,7 +257,7 @@ struct RouteShared {
   unsigned long long mask[MOE_DECODE_MAX_EXPERTS];
   int base[MOE_DECODE_MAX_EXPERTS];
   int wave_sum[kRouteWaves];
-  int picks[kOneLaunch * kMaxTopK];
+  int picks[kMaxChunk * kMaxTopK];
 };
 
 template <int kPer>
@@ -265,8 +276,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_one_kernel(moe_route_args
   place_routes(a, 0, a.T, sm.picks, sm.mask, sm.base);
 }
 
+// Two workgroups a CU where the logits of a lane leave registers for them (20.3
+// us with one, 18.2 with two, for 256 experts).
 template <int kPer>
-__global__ __launch_bounds__(kRouteThreads) void route_pick_kernel(moe_route_args a) {
+__global__ __launch_bounds__(kRouteThreads, kPer <= 4 ? 8 : 4) void route_pick_kernel(moe_route_args a) {
   __shared__ unsigned long long mask[MOE_DECODE_MAX_EXPERTS];
   const int chunk = chunk_tokens(a.T), t0 = blockIdx.x * chunk, n = min(chunk, a.T - t0);
   route_chunk<kPer>(a, t0, n, nullptr, mask);

@@ -44,8 +44,8 @@ def check(logits, bias, k, scale=2.5, **local):
     return r
 
 
-# tokens around the one-workgroup form (64) and a chunk's end; experts around each number per lane
-@pytest.mark.parametrize("T", [1, 2, 63, 64, 65, 127, 128, 129, 200])
+# tokens around the one-workgroup form (32) and the ends of chunks; experts around each number per lane
+@pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200])
 @pytest.mark.parametrize("E,k", [(8, 2), (256, 8)])
 def test_tokens(T, E, k):
     check(*make(T, E, T + E), k)
@@ -58,25 +58,25 @@ def test_experts(T, E, k):
     check(*make(T, E, 3 * T + E), k)
 
 
-@pytest.mark.parametrize("T", [64, 300])
+@pytest.mark.parametrize("T", [32, 300])
 def test_bf16_logits(T):
     check(*make(T, 200, 5, torch.bfloat16), 6, scale=1.0)
 
 
-@pytest.mark.parametrize("T", [40, 150])
+@pytest.mark.parametrize("T", [25, 150])
 @pytest.mark.parametrize("E,k", [(64, 8), (600, 16)])
 def test_equal_scores_go_to_the_lower_expert(T, E, k):
     check(*make(T, E, 6, ties=True), k)
 
 
-@pytest.mark.parametrize("T", [33, 150])
+@pytest.mark.parametrize("T", [30, 33, 150])
 @pytest.mark.parametrize("lb,lc", [(0, 8), (8, 24), (63, 1), (0, 64), (32, None)])
 def test_local_experts(T, lb, lc):
     r = check(*make(T, 64, 7), 4, local_begin=lb, local_experts=lc)
     assert r.offsets.shape[0] == (32 if lc is None else lc) + 1
 
 
-@pytest.mark.parametrize("T", [64, 200])
+@pytest.mark.parametrize("T", [32, 200])
 def test_one_expert_takes_all_and_one_none(T):
     logits, bias = make(T, 16, 8)
     bias[3], bias[5] = 50.0, -50.0
@@ -96,7 +96,7 @@ def test_infinite_logits():
 
 
 @pytest.mark.parametrize("mask", [float("-inf"), torch.finfo(torch.float32).min], ids=["infinity", "lowest"])
-@pytest.mark.parametrize("T", [40, 150])
+@pytest.mark.parametrize("T", [25, 150])
 def test_masked_experts(T, mask):
     """Experts switched off by their bias are not picked while k others are
     there, and are picked in their order where not."""
@@ -110,7 +110,7 @@ def test_masked_experts(T, mask):
     check(logits, bias, 8)
 
 
-@pytest.mark.parametrize("T", [40, 200])
+@pytest.mark.parametrize("T", [20, 200])
 def test_nan_logits_give_valid_places(T):
     """Whatever a NaN is routed to, every place is a row of the batch."""
     logits, bias = make(T, 32, 10)

@@ -94,8 +94,8 @@ def test_route_argument_errors(L, over, code):
 
 def test_route_workspace(L):
     """Nothing for a few tokens; it grows with tokens and experts."""
-    assert L.moe_route_rows_workspace(0, 8) == 0 and L.moe_route_rows_workspace(64, 1024) == 0
-    sizes = [L.moe_route_rows_workspace(T, 64) for T in (65, 100, 1000, 8192, 8193, 65536, 65537, 1048576)]
+    assert L.moe_route_rows_workspace(0, 8) == 0 and L.moe_route_rows_workspace(32, 1024) == 0
+    sizes = [L.moe_route_rows_workspace(T, 64) for T in (33, 65, 100, 1000, 8192, 8193, 65536, 65537, 1048576)]
     assert all(s >= 256 and s % 4 == 0 for s in sizes)
     assert L.moe_route_rows_workspace(1000, 128) == 2 * L.moe_route_rows_workspace(1000, 64)
     assert L.moe_route_rows_workspace(1048576, 1024) < 1 << 28
