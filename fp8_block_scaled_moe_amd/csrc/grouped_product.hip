@@ -67,7 +67,7 @@ __device__ __forceinline__ float4_t product(const int8v_t& w, const int8v_t& x, 
 // kJ: the most 16-row groups of a wave; `first`: those of the first four waves.
 template <bool kMx, int kRows, int kStages, bool kOnce, int kJ>
 __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared<kRows, kStages>& sm, int groups) {
-  constexpr int kHalf = kRows / 2;
+  constexpr int kHalf = kJ * kGroup;  // LDS rows of a half of the waves
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r16 = lane & 15, g = lane >> 4;
@@ -82,7 +82,9 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   // block and group are eight neighbouring columns and those of a row's four
   // lanes 32: instruction s has weight rows r of columns 32 (s / 2) +
   // 8 (r / 4) + 4 (s % 2) + r % 4.
-  constexpr int kXCopies = kRows / 64, kCopies = 4 + kXCopies + 1;
+  constexpr int kXCopies = (kJ + 1) / 2, kCopies = 4 + kXCopies + 1;
+  static_assert(kJ == 1 || kJ % 2 == 0, "whole copies of eight rows for each of eight waves (kJ = 1: for four)");
+  const int wx = kJ == 1 ? wave & 3 : wave * kXCopies;  // in eights of LDS rows
   const int lr = lane >> 3;
   const auto x_of = [&](int L) {  // activation row of LDS row L
     const int m = L % kHalf + L / kHalf * kGroup * first;
@@ -91,7 +93,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const uint8_t* xp[kXCopies];
 #pragma unroll
   for (int i = 0; i < kXCopies; ++i) {
-    const int L = (wave * kXCopies + i) * 8 + lr;
+    const int L = (wx + i) * 8 + lr;
     xp[i] = a.x + x_of(L) * a.K + ((lane & 7) ^ ((L >> 1) & 7)) * 16;
   }
   // its weight rows: 32 of the 64 columns of one wave; eight i begins at column
@@ -100,10 +102,10 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const uint8_t* wp = a.w + ((size_t)at.e * a.N + col) * a.K;
   const uint32_t wrow = (uint32_t)((lr >> 2) * 8 + (lr & 3)) * (uint32_t)a.K, chunk = ((lane & 7) ^ (lr >> 1)) * 16;
   const uint32_t woff[2] = {wrow + chunk, wrow + (chunk ^ 64)};
-  const int sl = wave % (kRows / 64) * 64;
+  const int sl = wave % kXCopies * 64;
   const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + x_of(sl + lane) * KB * 4;
   const uint32_t lds = lds_offset(&sm);
-  constexpr int kWCopies = 4, kRest = kXCopies + 1;
+  constexpr int kWCopies = 4;
   const auto issue_w = [&](int st, int kb) {
     const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kRows>);
     const size_t k0 = (size_t)kb * 128;
@@ -115,7 +117,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const auto issue_x = [&](int st, int kb) {
     const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kRows>);
 #pragma unroll
-    for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + (size_t)kb * 128, to + (wave * kXCopies + i) * 1024);
+    for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + (size_t)kb * 128, to + (wx + i) * 1024);
     copy4_to_lds(sp + (size_t)kb * 4, to + (uint32_t)offsetof(Stage<kRows>, xs) + sl * 4);
   };
 
@@ -235,20 +237,17 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_product_kernel(GroupedArg
   if (at.e < 0) return;
   const int groups = (at.end - at.row + kGroup - 1) / kGroup;
   const int need = (groups + 1) / 2;  // of the first half of the waves; the other half has the rest
-  if (kRows > 64) {
-    if (need > 6)
-      tile<kMx, kRows, kStages, kOnce, kRows / 32>(a, at, sm, groups);
-    else if (need > 4)
-      tile<kMx, kRows, kStages, kOnce, kRows / 32 < 6 ? kRows / 32 : 6>(a, at, sm, groups);
-    else if (need > 2)
-      tile<kMx, kRows, kStages, kOnce, kRows / 32 < 4 ? kRows / 32 : 4>(a, at, sm, groups);
-    else
-      tile<kMx, kRows, kStages, kOnce, 2>(a, at, sm, groups);
-  } else if (need > 1) {
+  constexpr int kMost = kRows / 32;
+  if (kMost > 6 && need > 6)
+    tile<kMx, kRows, kStages, kOnce, kMost>(a, at, sm, groups);
+  else if (kMost > 4 && need > 4)
+    tile<kMx, kRows, kStages, kOnce, kMost < 6 ? kMost : 6>(a, at, sm, groups);
+  else if (need > 2)
+    tile<kMx, kRows, kStages, kOnce, 4>(a, at, sm, groups);
+  else if (kMost > 4 || need > 1)
     tile<kMx, kRows, kStages, kOnce, 2>(a, at, sm, groups);
-  } else {
+  else
     tile<kMx, kRows, kStages, kOnce, 1>(a, at, sm, groups);
-  }
 }
 
 template <bool kMx, int kRows, int kStages, bool kOnce>
@@ -262,8 +261,8 @@ void launch(const GroupedArgs& a, hipStream_t stream) {
 void launch_grouped_product(bool mx, GroupedArgs a, hipStream_t stream) {
   a.col_tiles = (a.N + kCols - 1) / kCols;
   const int64_t R = a.R, E = a.E;
-  if (R <= E * 24)  // the mean rows of an expert: see above
-    mx ? launch<true, 64, 3, true>(a, stream) : launch<false, 64, 3, true>(a, stream);
+  if (R <= E * 56)  // the mean rows of an expert: see above
+    mx ? launch<true, 128, 3, true>(a, stream) : launch<false, 128, 3, true>(a, stream);
   else if (R <= E * 128)  // few experts have a second row tile (56 experts of 44 rows: 101 us with the hint, 104 without)
     mx ? launch<true, 256, 2, true>(a, stream) : launch<false, 256, 2, true>(a, stream);
   else
