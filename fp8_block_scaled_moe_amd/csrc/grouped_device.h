@@ -37,10 +37,11 @@ __device__ __forceinline__ uniform_ints as_uniform(const int32_t* p) { return (u
 void launch_grouped_product(bool mx, GroupedArgs a, hipStream_t stream);  // grouped_product.hip
 void launch_grouped_swiglu(bool mx, GroupedArgs a, hipStream_t stream);   // grouped_swiglu.hip
 
-// A workgroup's tile: grouped rows [row, end) of expert e, column tile `col`.
-// e < 0: no tile is left for it.
+// A workgroup's tile: grouped rows [row, end) of expert e, column tile `col`;
+// only: these are all of the expert's rows, so nobody else reads the tile's
+// weights. e < 0: no tile is left for it.
 struct TileAt {
-  int e, row, end, col;
+  int e, row, end, col, only;
 };
 
 // The workgroup's tile when every expert's rows are cut into as few tiles of
@@ -58,11 +59,11 @@ __device__ __forceinline__ TileAt find_tile(const GroupedArgs& a, int block) {
   constexpr int kPer = 1024 / kThreadsWg;  // experts per thread: E <= 1024
   static_assert(kPer >= 1, "every expert has a thread");
   __shared__ int wave_sum[kWavesWg];
-  __shared__ int found[4];
+  __shared__ int found[5];
   // R may be far more than the rows that are there (one GPU's share of the
   // experts): workgroups that these cannot need leave at once
   if ((unsigned)block >= grouped_workgroups(a, min(max(as_uniform(a.offsets)[a.E], 0), a.R), kRows))
-    return TileAt{-1, 0, 0, 0};
+    return TileAt{-1, 0, 0, 0, 0};
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int per = (a.E + kThreadsWg - 1) / kThreadsWg;
   const auto clamped = [&](int e) { return min(max(a.offsets[min(e, a.E)], 0), a.R); };
@@ -108,6 +109,7 @@ __device__ __forceinline__ TileAt find_tile(const GroupedArgs& a, int block) {
         found[1] = lo[q] + kGroup * (int)((int64_t)groups * i / tiles[q]);
         found[2] = min(lo[q] + kGroup * (int)((int64_t)groups * (i + 1) / tiles[q]), end);
         found[3] = mine / tiles[q];
+        found[4] = tiles[q] == 1;
       }
       before += tiles[q];
     }
@@ -118,6 +120,7 @@ __device__ __forceinline__ TileAt find_tile(const GroupedArgs& a, int block) {
   r.row = __builtin_amdgcn_readfirstlane(found[1]);
   r.end = __builtin_amdgcn_readfirstlane(found[2]);
   r.col = __builtin_amdgcn_readfirstlane(found[3]);
+  r.only = __builtin_amdgcn_readfirstlane(found[4]);
   return r;
 }
 
@@ -149,10 +152,10 @@ __device__ __forceinline__ void copy4_to_lds(const uint8_t* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform(to)), "v"(from));
 }
 // The same from a uniform address plus the lane's offset. kOnce: with the
-// non-temporal hint, for data that is read once (weights of one row tile: 16
-// rows for each of 64 experts of 4096 x 7168, 288 us with it and 318 without;
-// where row tiles share them, it costs: 65,536 rows over 256 such experts fetch
-// 13.8 GB with it and 9.6 without).
+// non-temporal hint, for data that is read once: weights of an expert's only
+// row tile (16 rows for each of 64 experts of 4096 x 7168, 288 us with it and
+// 318 without; where row tiles share them it costs: 65,536 rows over 256 such
+// experts, 4.92 ms with it and 4.69 without).
 template <bool kOnce>
 __device__ __forceinline__ void copy16_to_lds(const uint8_t* base, uint32_t offset, uint32_t to) {
   if (kOnce)

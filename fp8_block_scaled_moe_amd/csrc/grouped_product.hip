@@ -1,9 +1,9 @@
-// moe_grouped_gemm: up to 256 (64) rows of an expert by 256 weight rows per
+// moe_grouped_gemm: up to 256 rows of an expert by 256 weight rows per
 // workgroup, on the FP8 matrix instructions.
 //
 // Every 128-wide K block of the tile's activations and weights is copied into
-// LDS, read from there by eight waves, up to 128 (32) rows by 64 weight rows
-// each, and multiplied by the 16x16x128 instruction, a block's product per
+// LDS, read from there by eight waves, up to 128 rows by 64 weight rows each,
+// and multiplied by the 16x16x128 instruction, a block's product per
 // instruction; its FP32 sums are multiplied by the block's scales when they are
 // added. The instruction adds eight products at a time, each cut off 14 bits
 // below the power of two of the largest (measured one product at a time), and
@@ -16,16 +16,20 @@
 // The weights of a block are in registers from its beginning on, so their
 // place in LDS is refilled at once and the activations' place when they have
 // been read; the two halves of the waves share the tile's 16-row groups evenly
-// and a SIMD has a wave of each.
+// and a SIMD has a wave of each. A tile of up to 128 rows has three blocks in
+// LDS, a larger one two, and copies no more activation rows than its waves
+// read.
 //
 // Bounds, measured on MI355X. Few rows: the weights' bytes (one token, 8 experts,
-// N = 7168, K = 2048: 19.5 us, 6.0 TB/s; 16 rows for each of 64 experts: 5.9).
-// Many: the copies into LDS, 64 KB for 17 MFLOP, beside the matrix cores: 1.6
-// PFLOP/s for 512 rows for each of 64 experts, 1.9 without the copies; an FP8
-// library product without block scales reaches 2.7. Tiles of 64 rows, with
-// three blocks in LDS instead of two: 6% faster up to 20 rows an expert, as
-// fast at 28, 9% slower at 80.
+// N = 7168, K = 2048: 19.5 us, 6.0 TB/s; 2 rows for each of 64 experts: 6.1, 16:
+// 5.8, 28: 5.3, 64: 4.7). Many: the copies into LDS, 64 KB for 17 MFLOP, beside
+// the matrix cores: 1.6 PFLOP/s for 512 rows for each of 64 experts, 1.9 without
+// the copies; an FP8 library product without block scales reaches 2.7. Tiles of
+// at most 128 rows throughout: 3% faster for some 44 rows an expert, 5% slower
+// for 110.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "grouped_device.h"
 
@@ -34,18 +38,22 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kGroup = 16;  // rows of a matrix instruction
+constexpr int kRows = 256;  // of a tile, at most
 constexpr int kCols = 256;  // weight rows of a tile
 
-template <int kRows>
+// A K block in LDS, for waves of up to kJ 16-row groups.
+template <int kJ>
 struct Stage {
+  static constexpr int kRows = 2 * kJ * kGroup;
   uint8_t x[kRows * 128];
   uint8_t w[kCols * 128];
-  uint32_t xs[kRows];  // FP32 scales, or four E8M0 bytes
+  uint32_t xs[kRows < 64 ? 64 : kRows];  // FP32 scales, or four E8M0 bytes
 };
-template <int kRows, int kStages>
-struct Shared {
-  Stage<kRows> st[kStages];  // K blocks: one read, the others on their way
-};
+// Blocks in LDS: one read, the others on their way.
+template <int kJ>
+constexpr int kStages = kJ <= 4 ? 3 : 2;
+constexpr size_t kShared = kStages<4> * sizeof(Stage<4>);
+static_assert(kStages<8> * sizeof(Stage<8>) <= kShared && kShared <= 160 * 1024, "all forms fit");
 
 __device__ __forceinline__ int8v_t read_operand(const uint8_t* p, int lo, int hi) {
   const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p + lo), b = *reinterpret_cast<const u32x4_t*>(p + hi);
@@ -65,8 +73,9 @@ __device__ __forceinline__ float4_t product(const int8v_t& w, const int8v_t& x, 
 }
 
 // kJ: the most 16-row groups of a wave; `first`: those of the first four waves.
-template <bool kMx, int kRows, int kStages, bool kOnce, int kJ>
-__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared<kRows, kStages>& sm, int groups) {
+template <bool kMx, int kJ>
+__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, uint8_t* shared, int groups) {
+  Stage<kJ>* const sm = reinterpret_cast<Stage<kJ>*>(shared);
   constexpr int kHalf = kJ * kGroup;  // LDS rows of a half of the waves
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -104,21 +113,27 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const uint32_t woff[2] = {wrow + chunk, wrow + (chunk ^ 64)};
   const int sl = wave % kXCopies * 64;
   const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + x_of(sl + lane) * KB * 4;
-  const uint32_t lds = lds_offset(&sm);
+  const uint32_t lds = lds_offset(shared);
   constexpr int kWCopies = 4;
   const auto issue_w = [&](int st, int kb) {
-    const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kRows>);
+    const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kJ>);
     const size_t k0 = (size_t)kb * 128;
+    const auto all = [&](auto once) {
 #pragma unroll
-    for (int i = 0; i < kWCopies; ++i)
-      copy16_to_lds<kOnce>(wp + k0 + (size_t)((i & 1) * 16 + (i >> 1) * 4) * a.K, woff[i & 1],
-                    to + (uint32_t)offsetof(Stage<kRows>, w) + (wave * 32 + i * 8) * 128);
+      for (int i = 0; i < kWCopies; ++i)
+        copy16_to_lds<decltype(once)::value>(wp + k0 + (size_t)((i & 1) * 16 + (i >> 1) * 4) * a.K, woff[i & 1],
+                                             to + (uint32_t)offsetof(Stage<kJ>, w) + (wave * 32 + i * 8) * 128);
+    };
+    if (at.only)
+      all(std::true_type{});
+    else
+      all(std::false_type{});
   };
   const auto issue_x = [&](int st, int kb) {
-    const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kRows>);
+    const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kJ>);
 #pragma unroll
     for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + (size_t)kb * 128, to + (wx + i) * 1024);
-    copy4_to_lds(sp + (size_t)kb * 4, to + (uint32_t)offsetof(Stage<kRows>, xs) + sl * 4);
+    copy4_to_lds(sp + (size_t)kb * 4, to + (uint32_t)offsetof(Stage<kJ>, xs) + sl * 4);
   };
 
   const int n0 = at.col * kCols + wn * 64;
@@ -136,26 +151,26 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   // its weights are in registers from its beginning on, so their place is
   // filled anew at once; its activations' place when they have all been read.
 #pragma unroll
-  for (int b = 0; b < kStages; ++b)
+  for (int b = 0; b < kStages<kJ>; ++b)
     if (b < KB) {
       issue_w(b, b);
       issue_x(b, b);
     }
-  if (kStages - 1 < KB)
-    copies_left<(kStages - 1) * kCopies>(&sm);
+  if (kStages<kJ> - 1 < KB)
+    copies_left<(kStages<kJ> - 1) * kCopies>(shared);
   else
-    copies_left<0>(&sm);
+    copies_left<0>(shared);
   workgroup_barrier();
 
   int8v_t w[4], x[2];
   uint32_t sx[2];
   const auto load_w = [&](int st) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) w[s] = read_operand(sm.st[st].w + s * 2048, w_lo, w_lo ^ 64);
+    for (int s = 0; s < 4; ++s) w[s] = read_operand(sm[st].w + s * 2048, w_lo, w_lo ^ 64);
   };
   const auto load_x = [&](int st, int j) {
-    x[j & 1] = read_operand(sm.st[st].x + j * 2048, x_lo, x_lo ^ 64);
-    sx[j & 1] = sm.st[st].xs[wm * kHalf + j * 16 + r16];
+    x[j & 1] = read_operand(sm[st].x + j * 2048, x_lo, x_lo ^ 64);
+    sx[j & 1] = sm[st].xs[wm * kHalf + j * 16 + r16];
   };
   float4_t p[2][4];
   float sc[2];
@@ -177,10 +192,10 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   int st = 0;
   for (int b = 0; b < KB; ++b) {
     const float s0 = sw[b];
-    if (b + kStages < KB) {
+    if (b + kStages<kJ> < KB) {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       workgroup_barrier();  // every wave has read the block's weights
-      issue_w(st, b + kStages);
+      issue_w(st, b + kStages<kJ>);
     }
     // a group's scaled sums are added while the next group's instructions
     // run; the fences keep the compiler from loading further ahead than the
@@ -194,17 +209,17 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
     }
     if (b + 1 < KB) {
       // the next block is there, in every wave, and every wave has read all of this one
-      if (b + kStages < KB)
-        copies_left<(kStages - 2) * kCopies + kWCopies>(&sm);
+      if (b + kStages<kJ> < KB)
+        copies_left<(kStages<kJ> - 2) * kCopies + kWCopies>(shared);
       else
-        copies_left<0>(&sm);
+        copies_left<0>(shared);
       workgroup_barrier();
-      if (b + kStages < KB) issue_x(st, b + kStages);
+      if (b + kStages<kJ> < KB) issue_x(st, b + kStages<kJ>);
     }
     multiply(kJ - 1, s0);
     if (kJ > 1) add(kJ - 2);
     __builtin_amdgcn_sched_barrier(0);
-    st = st == kStages - 1 ? 0 : st + 1;
+    st = st == kStages<kJ> - 1 ? 0 : st + 1;
     if (b + 1 < KB) {
       load_w(st);
       load_x(st, 0);
@@ -230,43 +245,31 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   }
 }
 
-template <bool kMx, int kRows, int kStages, bool kOnce>
+template <bool kMx>
 __global__ __launch_bounds__(kThreads, 2) void grouped_product_kernel(GroupedArgs a) {
-  __shared__ Shared<kRows, kStages> sm;
+  __shared__ alignas(16) uint8_t shared[kShared];
   const TileAt at = find_tile<kRows, kGroup, kThreads>(a, blockIdx.x);
   if (at.e < 0) return;
   const int groups = (at.end - at.row + kGroup - 1) / kGroup;
   const int need = (groups + 1) / 2;  // of the first half of the waves; the other half has the rest
-  constexpr int kMost = kRows / 32;
-  if (kMost > 6 && need > 6)
-    tile<kMx, kRows, kStages, kOnce, kMost>(a, at, sm, groups);
-  else if (kMost > 4 && need > 4)
-    tile<kMx, kRows, kStages, kOnce, kMost < 6 ? kMost : 6>(a, at, sm, groups);
+  if (need > 6)
+    tile<kMx, 8>(a, at, shared, groups);
+  else if (need > 4)
+    tile<kMx, 6>(a, at, shared, groups);
   else if (need > 2)
-    tile<kMx, kRows, kStages, kOnce, 4>(a, at, sm, groups);
-  else if (kMost > 4 || need > 1)
-    tile<kMx, kRows, kStages, kOnce, 2>(a, at, sm, groups);
+    tile<kMx, 4>(a, at, shared, groups);
+  else if (need > 1)
+    tile<kMx, 2>(a, at, shared, groups);
   else
-    tile<kMx, kRows, kStages, kOnce, 1>(a, at, sm, groups);
-}
-
-template <bool kMx, int kRows, int kStages, bool kOnce>
-void launch(const GroupedArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((grouped_product_kernel<kMx, kRows, kStages, kOnce>), dim3(grouped_workgroups(a, a.R, kRows)), dim3(kThreads), 0,
-                     stream, a);
+    tile<kMx, 1>(a, at, shared, groups);
 }
 
 }  // namespace
 
 void launch_grouped_product(bool mx, GroupedArgs a, hipStream_t stream) {
   a.col_tiles = (a.N + kCols - 1) / kCols;
-  const int64_t R = a.R, E = a.E;
-  if (R <= E * 56)  // the mean rows of an expert: see above
-    mx ? launch<true, 128, 3, true>(a, stream) : launch<false, 128, 3, true>(a, stream);
-  else if (R <= E * 128)  // few experts have a second row tile (56 experts of 44 rows: 101 us with the hint, 104 without)
-    mx ? launch<true, 256, 2, true>(a, stream) : launch<false, 256, 2, true>(a, stream);
-  else
-    mx ? launch<true, 256, 2, false>(a, stream) : launch<false, 256, 2, false>(a, stream);
+  const auto kernel = mx ? grouped_product_kernel<true> : grouped_product_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3(grouped_workgroups(a, a.R, kRows)), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace moe

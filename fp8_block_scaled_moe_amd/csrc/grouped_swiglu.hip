@@ -2,7 +2,7 @@
 // weight rows, up and gate) per workgroup.
 //
 // Every 128-wide K block of the tile's activations and weights is copied into
-// LDS (48 KB, three blocks at a time), read from there by eight waves, 64 rows
+// LDS (up to 48 KB, three blocks at a time), read from there by eight waves, 64 rows
 // by 32 up and 32 gate columns each, widened to BF16 (exact) and multiplied by
 // the 32x32x16 instruction; the block's FP32 sums are multiplied by its scales
 // when they are added. BF16 and not the FP8 instruction, because the hidden's
@@ -15,13 +15,15 @@
 // a SIMD has one wave of each, and row tiles of an expert are alike in size.
 //
 // Bounds, measured on MI355X. Few rows: the weights' bytes (4 tokens x 8 of 256
-// experts, K = 7168, I = 2048: 138 us, 6.5 TB/s). Many: the matrix cores at the
+// experts, K = 7168, I = 2048: 134 us, 6.7 TB/s). Many: the matrix cores at the
 // clock that their power allows: 1.0 PFLOP/s for 4,096 rows for each of 8
 // experts (K = 7168), 1.23 without the copies, 1.3 in a loop of the same
 // instructions on registers; a BF16 library product reaches 1.22. Tiles of 32
 // rows with four blocks in LDS gained 1% below 5 rows an expert and lost 9%
 // at 12, so there is one size.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "grouped_device.h"
 
@@ -31,16 +33,17 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kGroup = 32;  // rows of a matrix instruction
 constexpr int kRows = 128;
-constexpr int kHalf = kRows / 2;  // of the LDS rows: a half of the waves
 constexpr int kStages = 3;        // K blocks in LDS: one read, the others on their way
 
+// A K block in LDS, for waves of up to kFirst 32-row groups.
+template <int kFirst>
 struct Stage {
-  uint8_t x[kRows * 128];
+  uint8_t x[2 * kFirst * kGroup * 128];
   uint8_t w[256 * 128];
-  uint32_t xs[kRows];  // FP32 scales, or four E8M0 bytes
+  uint32_t xs[2 * kFirst * kGroup];  // FP32 scales, or four E8M0 bytes
 };
 struct Shared {
-  Stage st[kStages];
+  alignas(16) uint8_t st[kStages * sizeof(Stage<2>)];
   float amax[4][kRows];
 };
 
@@ -54,9 +57,11 @@ __device__ __forceinline__ Wide16 widen16(const u32x4_t& q, float scale) {
   return Wide16{{widen8_scaled(q[0], q[1], scale), widen8_scaled(q[2], q[3], scale)}};
 }
 
-// kJ: the 32-row groups of this wave; `first`: those of the first four waves.
-template <bool kMx, bool kOnce, int kJ>
-__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared& sm, int first) {
+// kJ: the 32-row groups of this wave; kFirst: those of the first four waves.
+template <bool kMx, int kFirst, int kJ>
+__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared& sm) {
+  constexpr int kHalf = kFirst * kGroup;  // LDS rows of a half of the waves
+  const Stage<kFirst>* const stage = reinterpret_cast<const Stage<kFirst>*>(sm.st);
   constexpr int kN = kJ ? kJ : 1;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -71,16 +76,15 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   // bank. A wave's results of an instruction are weight rows 8 a + 4 h + b (a,
   // b = 0..3) of its 32: these are columns 16 h + 4 a + b, so that a lane's 16
   // are neighbours.
-  constexpr int kXCopies = 2, kCopies = 4 + kXCopies + 1;
+  constexpr int kXCopies = kFirst, kCopies = 4 + kXCopies + 1;
   const int lr = lane >> 3;
   const auto x_of = [&](int L) {  // activation row of LDS row L
-    const int m = L % kHalf + L / kHalf * kGroup * first;
-    return (size_t)max(x_row(a, min(at.row + m, at.end - 1)), 0);
+    return (size_t)max(x_row(a, min(at.row + L, at.end - 1)), 0);
   };
   const uint8_t* xp[kXCopies];
 #pragma unroll
   for (int i = 0; i < kXCopies; ++i) {
-    const int L = wave * 16 + i * 8 + lr;
+    const int L = (wave * kXCopies + i) * 8 + lr;
     xp[i] = a.x + x_of(L) * a.K + ((lane & 7) ^ ((L >> 1) & 7)) * 16;
   }
   // up rows for even waves, the same columns' gate rows for odd ones; its
@@ -89,19 +93,25 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const uint8_t* wp = a.w + ((size_t)at.e * a.N + at.col * 128 + (wave >> 1) * 32 + (wave & 1) * I) * a.K;
   const uint32_t wrow = (uint32_t)((lr >> 2) * 16 + (lr & 3)) * (uint32_t)a.K, chunk = ((lane & 7) ^ (lr >> 1)) * 16;
   const uint32_t woff[2] = {wrow + chunk, wrow + (chunk ^ 64)};
-  const int sl = (wave & 1) * 64;  // its first scale
+  const int sl = wave % kFirst * 64;  // its first scale
   const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + x_of(sl + lane) * KB * 4;
-  const uint32_t lds = lds_offset(&sm);
+  const uint32_t lds = lds_offset(sm.st);
   const auto issue = [&](int st, int kb) {
-    const uint32_t to = lds + st * (uint32_t)sizeof(Stage);
+    const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kFirst>);
     const size_t k0 = (size_t)kb * 128;
+    const auto weights = [&](auto once) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      copy16_to_lds<kOnce>(wp + k0 + (size_t)(4 * i) * a.K, woff[i & 1],
-                    to + (uint32_t)offsetof(Stage, w) + (wave * 32 + i * 8) * 128);
+      for (int i = 0; i < 4; ++i)
+        copy16_to_lds<decltype(once)::value>(wp + k0 + (size_t)(4 * i) * a.K, woff[i & 1],
+                                             to + (uint32_t)offsetof(Stage<kFirst>, w) + (wave * 32 + i * 8) * 128);
+    };
+    if (at.only)
+      weights(std::true_type{});
+    else
+      weights(std::false_type{});
 #pragma unroll
-    for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + k0, to + (wave * 16 + i * 8) * 128);
-    copy4_to_lds(sp + (size_t)kb * 4, to + (uint32_t)offsetof(Stage, xs) + sl * 4);
+    for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + k0, to + (wave * kXCopies + i) * 1024);
+    copy4_to_lds(sp + (size_t)kb * 4, to + (uint32_t)offsetof(Stage<kFirst>, xs) + sl * 4);
   };
 
   const uniform_floats su = as_uniform(a.ws) + ((size_t)at.e * (a.N / 128) + at.col) * KB;
@@ -122,7 +132,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const auto scales = [&](int st) {
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
-      const uint32_t sx = sm.st[st].xs[wm * kHalf + j * 32 + r32];
+      const uint32_t sx = stage[st].xs[wm * kHalf + j * 32 + r32];
 #pragma unroll
       for (int c = 0; c < 4; ++c) rel[j][c] = 1.f;
       xs[j] = kMx ? mx_scales(sx, rel[j]) : __uint_as_float(sx);
@@ -130,7 +140,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   };
   const auto load = [&](int st, int c) {
     if (!kJ) return;
-    const uint8_t *wb = sm.st[st].w + wn * 64 * 128, *xb = sm.st[st].x + wm * kHalf * 128;
+    const uint8_t *wb = stage[st].w + wn * 64 * 128, *xb = stage[st].x + wm * kHalf * 128;
 #pragma unroll
     for (int t = 0; t < 2; ++t) w[c & 1][t] = widen16(*reinterpret_cast<const u32x4_t*>(wb + t * 4096 + off[c]), 1.f);
 #pragma unroll
@@ -213,7 +223,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kJ; ++j) {
-    const int i = at.row + (wm * first + j) * kGroup + r32;
+    const int i = at.row + (wm * kFirst + j) * kGroup + r32;
     if (i < at.end) {
       float amax = kAmaxFloor;
 #pragma unroll
@@ -233,32 +243,33 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   }
 }
 
-template <bool kMx, bool kOnce>
+template <bool kMx>
 __global__ __launch_bounds__(kThreads, 2) void grouped_swiglu_kernel(GroupedArgs a) {
   __shared__ Shared sm;
   const TileAt at = find_tile<kRows, kGroup, kThreads>(a, blockIdx.x);
   if (at.e < 0) return;
-  // the first half of the waves takes `first` of the 32-row groups, the other
-  // the rest; all branches meet the same barriers
+  // the first half of the waves takes half of the 32-row groups, rounded up,
+  // the other the rest; all branches meet the same barriers
   const int groups = (at.end - at.row + kGroup - 1) / kGroup, first = (groups + 1) / 2;
-  const int mine = threadIdx.x < kThreads / 2 ? first : groups - first;
-  if (mine == 2)
-    tile<kMx, kOnce, 2>(a, at, sm, first);
-  else if (mine == 1)
-    tile<kMx, kOnce, 1>(a, at, sm, first);
-  else
-    tile<kMx, kOnce, 0>(a, at, sm, first);
+  const bool half = threadIdx.x < kThreads / 2;
+  if (first == 2) {
+    if (half || groups == 4)
+      tile<kMx, 2, 2>(a, at, sm);
+    else
+      tile<kMx, 2, 1>(a, at, sm);
+  } else if (half || groups == 2) {
+    tile<kMx, 1, 1>(a, at, sm);
+  } else {
+    tile<kMx, 1, 0>(a, at, sm);
+  }
 }
 
 }  // namespace
 
 void launch_grouped_swiglu(bool mx, GroupedArgs a, hipStream_t stream) {
   a.col_tiles = a.N / 256;
-  const dim3 grid(grouped_workgroups(a, a.R, kRows));
-  const bool once = (int64_t)a.R <= (int64_t)a.E * 64;  // few experts have a second row tile
-  const auto kernel = mx ? (once ? grouped_swiglu_kernel<true, true> : grouped_swiglu_kernel<true, false>)
-                         : (once ? grouped_swiglu_kernel<false, true> : grouped_swiglu_kernel<false, false>);
-  hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);
+  const auto kernel = mx ? grouped_swiglu_kernel<true> : grouped_swiglu_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3(grouped_workgroups(a, a.R, kRows)), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace moe
