@@ -2,23 +2,26 @@
 // weight rows, up and gate) per workgroup.
 //
 // Every 128-wide K block of the tile's activations and weights is copied into
-// LDS (up to 48 KB, three blocks at a time), read from there by eight waves, 64 rows
-// by 32 up and 32 gate columns each, widened to BF16 (exact) and multiplied by
-// the 32x32x16 instruction; the block's FP32 sums are multiplied by its scales
-// when they are added. BF16 and not the FP8 instruction, because the hidden's
-// codes and scales are decided from these sums: the FP8 instruction adds eight
-// products at a time cut off 14 bits below the largest (measured; 2^-16 of a
-// result on average), which moves an FP32 scale by 1e-5, ten times what FP32
-// sums do. F16 is as exact (24 bits below the largest, both) for FP32 scales, a
-// hundredth slower (4.61 and 4.56 ms for 65,536 rows over 256 experts, K = 7168,
-// I = 2048), and too narrow for MXFP8 scales that lie 2^15 and more apart. The two halves of the waves share the tile's 32-row groups evenly,
-// a SIMD has one wave of each, and row tiles of an expert are alike in size.
+// LDS (up to 48 KB, three blocks at a time), read from there by eight waves, 64
+// rows by 32 up and 32 gate columns each, widened to BF16 (exact) and multiplied
+// by the 32x32x16 instruction; the block's FP32 sums are multiplied by its
+// scales when they are added. BF16 and not the FP8 instruction, because the
+// hidden's codes and scales are decided from these sums: the FP8 instruction
+// adds eight products at a time cut off 14 bits below the largest (measured;
+// 2^-16 of a result on average), which moves an FP32 scale by 1e-5, ten times
+// what FP32 sums do. F16 is as exact (both keep 23 bits below the largest), but
+// a hundredth slower (4.61 and 4.56 ms for 65,536 rows over 256 experts, K =
+// 7168, I = 2048) and too narrow for MXFP8 scales that lie 2^15 and more apart.
+// The two halves of the waves share the tile's 32-row groups evenly, a SIMD has
+// one wave of each, and row tiles of an expert are alike in size.
 //
 // Bounds, measured on MI355X. Few rows: the weights' bytes (4 tokens x 8 of 256
-// experts, K = 7168, I = 2048: 134 us, 6.7 TB/s). Many: the matrix cores at the
-// clock that their power allows: 1.0 PFLOP/s for 4,096 rows for each of 8
-// experts (K = 7168), 1.23 without the copies, 1.3 in a loop of the same
-// instructions on registers; a BF16 library product reaches 1.22. Tiles of 32
+// experts, K = 7168, I = 2048: 134 us, 6.7 TB/s). Many: the matrix
+// instructions with the 8 vector instructions that each needs (widening, scaled
+// sums), 45% and 48% of the cycles at the 1.8-2.0 GHz that their power allows:
+// 1.0 PFLOP/s for 4,096 rows for each of 8 experts (K = 7168), 1.23 without the
+// copies, 1.3 in a loop of the same instructions on registers; a BF16 library
+// product reaches 1.22. Tiles of 32
 // rows with four blocks in LDS gained 1% below 5 rows an expert and lost 9%
 // at 12, so there is one size.
 #include <hip/hip_runtime.h>
@@ -32,8 +35,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kGroup = 32;  // rows of a matrix instruction
-constexpr int kRows = 128;
-constexpr int kStages = 3;        // K blocks in LDS: one read, the others on their way
+constexpr int kRows = 128;  // of a tile, at most
+constexpr int kStages = 3;  // K blocks in LDS: one read, the others on their way
 
 // A K block in LDS, for waves of up to kFirst 32-row groups.
 template <int kFirst>
