@@ -19,6 +19,8 @@ from ._capi import DTYPE_BF16, DTYPE_F32, MoeDecodeError, OK, _FP8, _need, lib
 
 QUANT = {None: 0, "fp8": 1, "fp8_p2": 2, "mxfp8": 3}
 ROWS_MAX_D = 16384
+ROWS_MAX_TOKENS = 1048576
+_I32_MAX = 2**31 - 1  # sizes are 32-bit integers in the C ABI
 
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
@@ -149,6 +151,8 @@ def add_rmsnorm_quant(residual: Optional[torch.Tensor], gamma: Optional[torch.Te
         raise ValueError("at least one of residual, delta and routed rows (y, pos, weights) is needed")
     if inplace and (residual is None or not want_residual):
         raise ValueError("inplace needs a residual to update")
+    if T > ROWS_MAX_TOKENS:
+        raise ValueError(f"at most {ROWS_MAX_TOKENS} tokens, got {T}")
     dev = like.device
     rp = None if residual is None else _arg(residual, "residual", _BF16, dev, (T, D))
     dp = None if delta is None else _arg(delta, "delta", _BF16, dev, (T, D))
@@ -159,6 +163,8 @@ def add_rmsnorm_quant(residual: Optional[torch.Tensor], gamma: Optional[torch.Te
         if not isinstance(y, torch.Tensor) or y.dim() != 2 or not isinstance(pos, torch.Tensor) or pos.dim() != 2:
             raise ValueError("routed rows need y [R, D], pos [T, k] and weights [T, k]")
         R, k = y.shape[0], pos.shape[1]
+        if R > _I32_MAX:
+            raise ValueError(f"y has {R} rows, at most 2^31 - 1 are supported")
         yp = _arg(y, "y", _BF16, dev, (R, D))
         pp = _arg(pos, "pos", _I32, dev, (T, k), 4)
         wp = _arg(weights, "weights", _F32, dev, (T, k), 4)
@@ -196,6 +202,8 @@ def route_rows(logits: torch.Tensor, bias: torch.Tensor, *, top_k: int, routed_s
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a [T, E] tensor")
     T, E = logits.shape
+    if T > ROWS_MAX_TOKENS:
+        raise ValueError(f"at most {ROWS_MAX_TOKENS} tokens, got {T}")
     dev = logits.device
     lp = _arg(logits, "logits", (torch.float32, torch.bfloat16), dev, (T, E), 2 if logits.dtype == torch.bfloat16 else 4)
     bp = _arg(bias, "bias", _F32, dev, (E,), 4)
@@ -230,6 +238,10 @@ def _grouped(x, x_scale, w, w_scale, offsets, rows):
         raise ValueError(f"K and N must be multiples of 128 and 1 <= E <= 1024, got E={E}, N={N}, K={K}")
     if not isinstance(x_scale, torch.Tensor):
         raise ValueError("x_scale must be a tensor")
+    if rows is not None and (not isinstance(rows, torch.Tensor) or rows.dim() != 1):
+        raise ValueError("rows must be an [R] tensor")
+    if max(X, N, K, 0 if rows is None else rows.shape[0]) > _I32_MAX:
+        raise ValueError("rows and columns are limited to 2^31 - 1")
     mx = x_scale.dtype != torch.float32
     xp = _arg(x, "x", _FP8, dev, (X, K))
     sp = _arg(x_scale, "x_scale", _U8 if mx else _F32, dev, (X, K // 32 if mx else K // 128), 4)
@@ -238,8 +250,6 @@ def _grouped(x, x_scale, w, w_scale, offsets, rows):
     op = _arg(offsets, "offsets", _I32, dev, (E + 1,), 4)
     rp, R = None, X
     if rows is not None:
-        if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
-            raise ValueError("rows must be an [R] tensor")
         R = rows.shape[0]
         rp = _arg(rows, "rows", _I32, dev, (R,), 4)
         if R and not X:

@@ -20,7 +20,8 @@
  * and calls on different streams are independent (each moe_route_rows call in
  * flight needs its own workspace).
  *
- * All pointers are device pointers, arrays row-major and contiguous. Nothing
+ * All pointers are device pointers, arrays row-major and contiguous; outputs
+ * overlap no input (but for residual_out, below) and no other output. Nothing
  * is enqueued on an error: INVALID_ARG (negative size, NULL or misaligned
  * pointer, bad value), UNSUPPORTED (sizes or options outside the limits),
  * HIP (launch failure).
@@ -76,7 +77,7 @@ extern "C" {
  *   out          [T, D] BF16 or NULL
  *   q            [T, D] e4m3 and scale [T, D/128] FP32 or [T, D/32] bytes
  *                (by `quant`); both NULL with MOE_QUANT_NONE
- * No other overlap of outputs with inputs. BF16 and e4m3 arrays 16-byte
+ * BF16 and e4m3 arrays 16-byte
  * aligned, the others to their element. D a multiple of 128 (FP8), 32 (MXFP8)
  * or 8 (no quantisation) up to MOE_ROWS_MAX_D; T <= MOE_ROWS_MAX_TOKENS;
  * 0 <= k <= 32; eps >= 0, finite. At least one output and at least one of residual, delta, y.

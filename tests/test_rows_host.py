@@ -192,6 +192,27 @@ def test_binding_needs_a_gpu():
         pkg.grouped_swiglu(*grouped_args(), limit=7.0)
 
 
+def test_sizes_past_32_bits_are_refused():
+    """Lengths that the C ABI's 32-bit sizes would cut off (views of one row:
+    nothing is allocated)."""
+    many = 2**32 + 1
+    long = lambda t: t.expand(many, *t.shape[1:])  # noqa: E731
+    with pytest.raises(ValueError, match="tokens"):
+        pkg.add_rmsnorm_quant(long(torch.zeros(1, 8, dtype=BF)), None, quant=None)
+    with pytest.raises(ValueError, match="tokens"):
+        pkg.route_rows(long(torch.zeros(1, 8)), torch.zeros(8), top_k=1, routed_scale=1.0)
+    with pytest.raises(ValueError, match="rows"):
+        pkg.add_rmsnorm_quant(**{**norm_args(), "y": long(torch.zeros(1, 256, dtype=BF))})
+    for i in (0, 1):
+        args = grouped_args()
+        args[0] = long(torch.zeros(1, 256, dtype=torch.uint8)) if i == 0 else args[0]
+        rows = long(torch.zeros(1, dtype=torch.int32)) if i else None
+        with pytest.raises(ValueError, match="2\\^31"):
+            pkg.grouped_gemm(*args, rows=rows)
+        with pytest.raises(ValueError, match="2\\^31"):
+            pkg.grouped_swiglu(*args, rows=rows, limit=7.0)
+
+
 @pytest.mark.parametrize("args,kw", [
     ((torch.zeros(8), torch.zeros(8)), dict(top_k=2)),
     ((torch.zeros(2, 8).double(), torch.zeros(8)), dict(top_k=2)),
