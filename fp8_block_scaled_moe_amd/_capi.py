@@ -139,6 +139,9 @@ def lib() -> ctypes.CDLL:
         getattr(L, name).restype = ctypes.c_int
     L.moe_route_rows_workspace.argtypes = [i32, i32]
     L.moe_route_rows_workspace.restype = sz
+    for name in ("moe_grouped_gemm_workspace", "moe_grouped_swiglu_workspace"):
+        getattr(L, name).argtypes = [i32, i32, i32, i32]
+        getattr(L, name).restype = sz
     _lib = L
     return L
 

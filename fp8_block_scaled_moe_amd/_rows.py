@@ -2,7 +2,7 @@
 tokens, as separate calls.
 
 Argument checks and marshalling only. Every call allocates its outputs (and
-route_rows its workspace) from torch's caching allocator and launches on the
+route_rows and the grouped products their workspace) from torch's caching allocator and launches on the
 current stream of the tensors' device, or on `stream` when one is given; it
 never synchronises, so it can be captured into a graph.
 """
@@ -45,7 +45,8 @@ class RouteArgs(ctypes.Structure):
 class GroupedArgs(ctypes.Structure):
     _fields_ = [("R", _i32), ("X", _i32), ("E", _i32), ("N", _i32), ("K", _i32), ("quant", _i32),
                 ("limit", _f32), ("x", _vp), ("x_scale", _vp), ("rows", _vp),
-                ("offsets", _vp), ("w", _vp), ("w_scale", _vp), ("out", _vp), ("out_scale", _vp)]
+                ("offsets", _vp), ("w", _vp), ("w_scale", _vp), ("out", _vp), ("out_scale", _vp), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t)]
 
 
 class RoutedRows(NamedTuple):
@@ -271,7 +272,10 @@ def grouped_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scal
     with _where(dev, stream):
         out = torch.empty((R, sizes[3]), dtype=torch.bfloat16, device=dev)
         if R:
-            _call("moe_grouped_gemm", GroupedArgs(*sizes, 0.0, *ptrs, out.data_ptr(), None), dev)
+            need = lib().moe_grouped_gemm_workspace(R, *sizes[2:5])
+            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+            _call("moe_grouped_gemm", GroupedArgs(*sizes, 0.0, *ptrs, out.data_ptr(), None,
+                                                  None if ws is None else ws.data_ptr(), need), dev)
     return out
 
 
@@ -291,5 +295,8 @@ def grouped_swiglu(x: torch.Tensor, x_scale: torch.Tensor, w13: torch.Tensor, w1
         h = torch.empty((R, I), dtype=torch.uint8, device=dev)
         scale = torch.empty((R, I // 128), dtype=torch.float32, device=dev)
         if R:
-            _call("moe_grouped_swiglu", GroupedArgs(*sizes, limit, *ptrs, h.data_ptr(), scale.data_ptr()), dev)
+            need = lib().moe_grouped_swiglu_workspace(R, *sizes[2:5])
+            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+            _call("moe_grouped_swiglu", GroupedArgs(*sizes, limit, *ptrs, h.data_ptr(), scale.data_ptr(),
+                                                    None if ws is None else ws.data_ptr(), need), dev)
     return h, scale

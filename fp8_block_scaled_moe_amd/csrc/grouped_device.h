@@ -17,8 +17,19 @@ struct GroupedArgs {
   float* outs;
   int R, X, E, N, K;
   float limit;
-  int col_tiles;  // column tiles of an expert's output
+  int splits;      // parts of K, one per workgroup
+  float* partial;  // [splits][R][N] FP32 sums over a part of K each, where splits > 1
+  int col_tiles;   // column tiles of an expert's output times `splits`
 };
+
+// Parts of K for so few tiles (of up to `rows` rows by 256 weight rows) that
+// they leave CUs idle: as many as give every CU a part, of four 128-wide blocks
+// and more. See grouped_gemm.hip.
+inline int grouped_splits(int R, int E, int N, int K, int rows) {
+  const int64_t full = (int64_t)R / rows + E, tiles = (full < R ? full : R) * ((N + 255) / 256);
+  const int64_t most = K / 128 / 4, wanted = tiles > 0 ? 256 / tiles : 1;
+  return (int)(wanted < 2 || most < 2 ? 1 : wanted < most ? wanted : most);
+}
 
 // Workgroups that find_tile's tiles need at most for R grouped rows (each
 // expert's rows rounded up, no tile without a row), a multiple of the XCDs.
@@ -34,15 +45,28 @@ typedef const __attribute__((address_space(4))) int32_t* uniform_ints;
 __device__ __forceinline__ uniform_floats as_uniform(const float* p) { return (uniform_floats)(uintptr_t)p; }
 __device__ __forceinline__ uniform_ints as_uniform(const int32_t* p) { return (uniform_ints)(uintptr_t)p; }
 
+constexpr int kProductRows = 256, kSwigluRows = 128;                      // of a tile, at most
 void launch_grouped_product(bool mx, GroupedArgs a, hipStream_t stream);  // grouped_product.hip
 void launch_grouped_swiglu(bool mx, GroupedArgs a, hipStream_t stream);   // grouped_swiglu.hip
 
-// A workgroup's tile: grouped rows [row, end) of expert e, column tile `col`;
+// A workgroup's tile: grouped rows [row, end) of expert e, column tile and
+// part of K `col`;
 // only: these are all of the expert's rows, so nobody else reads the tile's
 // weights. e < 0: no tile is left for it.
 struct TileAt {
   int e, row, end, col, only;
 };
+
+// A workgroup's part of K, in 128-wide blocks.
+struct KPart {
+  int split, first, blocks;
+};
+__device__ __forceinline__ KPart k_part(const GroupedArgs& a, const TileAt& at) {
+  const int KB = a.K / 128, split = at.col % a.splits;
+  const int lo = KB * split / a.splits;
+  return KPart{split, lo, KB * (split + 1) / a.splits - lo};
+}
+
 
 // The workgroup's tile when every expert's rows are cut into as few tiles of
 // at most kRows (a multiple of kGroup) as can be, even but for kGroup rows.

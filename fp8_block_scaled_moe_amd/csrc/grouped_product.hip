@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kGroup = 16;  // rows of a matrix instruction
-constexpr int kRows = 256;  // of a tile, at most
+constexpr int kRows = kProductRows;
 constexpr int kCols = 256;  // weight rows of a tile
 
 // A K block in LDS, for waves of up to kJ 16-row groups.
@@ -81,7 +81,9 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, uin
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r16 = lane & 15, g = lane >> 4;
   const int wn = wave & 3, wm = wave >> 2;
-  const int KB = a.K / 128, first = (groups + 1) / 2;
+  const int first = (groups + 1) / 2, tile_col = at.col / a.splits;
+  const KPart part = k_part(a, at);
+  const int KB = part.blocks;
 
   // What this wave copies of a block: 32 LDS rows of the weights, kRows / 8 of
   // the activations, 64 scales (the same ones by several waves, so that every
@@ -103,16 +105,16 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, uin
 #pragma unroll
   for (int i = 0; i < kXCopies; ++i) {
     const int L = (wx + i) * 8 + lr;
-    xp[i] = a.x + x_of(L) * a.K + ((lane & 7) ^ ((L >> 1) & 7)) * 16;
+    xp[i] = a.x + x_of(L) * a.K + (size_t)part.first * 128 + ((lane & 7) ^ ((L >> 1) & 7)) * 16;
   }
   // its weight rows: 32 of the 64 columns of one wave; eight i begins at column
   // 16 (i % 2) + 4 (i / 2) and, where i is odd, at the other half's chunks
-  const int col = min(at.col * kCols + (wave >> 1) * 64, a.N - 64) + (wave & 1) * 32;
-  const uint8_t* wp = a.w + ((size_t)at.e * a.N + col) * a.K;
+  const int col = min(tile_col * kCols + (wave >> 1) * 64, a.N - 64) + (wave & 1) * 32;
+  const uint8_t* wp = a.w + ((size_t)at.e * a.N + col) * a.K + (size_t)part.first * 128;
   const uint32_t wrow = (uint32_t)((lr >> 2) * 8 + (lr & 3)) * (uint32_t)a.K, chunk = ((lane & 7) ^ (lr >> 1)) * 16;
   const uint32_t woff[2] = {wrow + chunk, wrow + (chunk ^ 64)};
   const int sl = wave % kXCopies * 64;
-  const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + x_of(sl + lane) * KB * 4;
+  const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + (x_of(sl + lane) * (a.K / 128) + part.first) * 4;
   const uint32_t lds = lds_offset(shared);
   constexpr int kWCopies = 4;
   const auto issue_w = [&](int st, int kb) {
@@ -136,8 +138,8 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, uin
     copy4_to_lds(sp + (size_t)kb * 4, to + (uint32_t)offsetof(Stage<kJ>, xs) + sl * 4);
   };
 
-  const int n0 = at.col * kCols + wn * 64;
-  const uniform_floats sw = as_uniform(a.ws) + ((size_t)at.e * (a.N / 128) + min(n0, a.N - 1) / 128) * KB;
+  const int n0 = tile_col * kCols + wn * 64;
+  const uniform_floats sw = as_uniform(a.ws) + ((size_t)at.e * (a.N / 128) + min(n0, a.N - 1) / 128) * (a.K / 128) + part.first;
   const int swz = (g ^ (r16 >> 1)) * 16;
   const int w_lo = (wn * 64 + r16) * 128 + swz, x_lo = (wm * kHalf + r16) * 128 + swz;
 
@@ -232,6 +234,12 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, uin
   for (int j = 0; j < kJ; ++j) {
     const int i = at.row + (wm * first + j) * kGroup + r16;
     if (j < (wm ? groups - first : first) && i < at.end) {
+      if (a.splits > 1) {
+        float* o = a.partial + ((size_t)part.split * a.R + i) * a.N + n0 + g * 8;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) *reinterpret_cast<float4_t*>(o + 32 * (s >> 1) + 4 * (s & 1)) = acc[j][s];
+        continue;
+      }
       const bool none = x_row(a, i) < 0;
       uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)i * a.N + n0 + g * 8;
 #pragma unroll
@@ -267,7 +275,7 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_product_kernel(GroupedArg
 }  // namespace
 
 void launch_grouped_product(bool mx, GroupedArgs a, hipStream_t stream) {
-  a.col_tiles = (a.N + kCols - 1) / kCols;
+  a.col_tiles = (a.N + kCols - 1) / kCols * a.splits;
   const auto kernel = mx ? grouped_product_kernel<true> : grouped_product_kernel<false>;
   hipLaunchKernelGGL(kernel, dim3(grouped_workgroups(a, a.R, kRows)), dim3(kThreads), 0, stream, a);
 }

@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kGroup = 32;  // rows of a matrix instruction
-constexpr int kRows = 128;  // of a tile, at most
+constexpr int kRows = kSwigluRows;
 constexpr int kStages = 3;  // K blocks in LDS: one read, the others on their way
 
 // A K block in LDS, for waves of up to kFirst 32-row groups.
@@ -70,7 +70,9 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r32 = lane & 31, h = lane >> 5;
   const int wn = wave & 3, wm = wave >> 2;
-  const int KB = a.K / 128, I = a.N / 2;
+  const int I = a.N / 2, tile_col = at.col / a.splits;
+  const KPart part = k_part(a, at);
+  const int KB = part.blocks;
 
   // What this wave copies of a block: 32 LDS rows of the weights, 16 of the
   // activations and 64 scales (the same ones by four waves each, so that every
@@ -88,16 +90,16 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
 #pragma unroll
   for (int i = 0; i < kXCopies; ++i) {
     const int L = (wave * kXCopies + i) * 8 + lr;
-    xp[i] = a.x + x_of(L) * a.K + ((lane & 7) ^ ((L >> 1) & 7)) * 16;
+    xp[i] = a.x + x_of(L) * a.K + (size_t)part.first * 128 + ((lane & 7) ^ ((L >> 1) & 7)) * 16;
   }
   // up rows for even waves, the same columns' gate rows for odd ones; its
   // eight LDS rows i begin 4 i columns further, at the other half's chunks
   // where i is odd
-  const uint8_t* wp = a.w + ((size_t)at.e * a.N + at.col * 128 + (wave >> 1) * 32 + (wave & 1) * I) * a.K;
+  const uint8_t* wp = a.w + ((size_t)at.e * a.N + tile_col * 128 + (wave >> 1) * 32 + (wave & 1) * I) * a.K + (size_t)part.first * 128;
   const uint32_t wrow = (uint32_t)((lr >> 2) * 16 + (lr & 3)) * (uint32_t)a.K, chunk = ((lane & 7) ^ (lr >> 1)) * 16;
   const uint32_t woff[2] = {wrow + chunk, wrow + (chunk ^ 64)};
   const int sl = wave % kFirst * 64;  // its first scale
-  const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + x_of(sl + lane) * KB * 4;
+  const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + (x_of(sl + lane) * (a.K / 128) + part.first) * 4;
   const uint32_t lds = lds_offset(sm.st);
   const auto issue = [&](int st, int kb) {
     const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kFirst>);
@@ -117,8 +119,8 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
     copy4_to_lds(sp + (size_t)kb * 4, to + (uint32_t)offsetof(Stage<kFirst>, xs) + sl * 4);
   };
 
-  const uniform_floats su = as_uniform(a.ws) + ((size_t)at.e * (a.N / 128) + at.col) * KB;
-  const uniform_floats sg = su + (size_t)(I / 128) * KB;
+  const uniform_floats su = as_uniform(a.ws) + ((size_t)at.e * (a.N / 128) + tile_col) * (a.K / 128) + part.first;
+  const uniform_floats sg = su + (size_t)(I / 128) * (a.K / 128);
 
   // Sixteen bytes of every row (chunk h + 2 c of the lane's row) at a time,
   // widened while the matrix instructions of the chunk before run. Of a
@@ -209,6 +211,23 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
         for (int i = 0; i < 16; ++i) acc[j][t][i] = fmaf(p[j][t][i], sc[j][t], acc[j][t][i]);
   }
 
+  if (a.splits > 1) {
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      const int i = at.row + (wm * kFirst + j) * kGroup + r32;
+      if (i < at.end) {
+        float* o = a.partial + ((size_t)part.split * a.R + i) * a.N + tile_col * 128 + wn * 32 + h * 16;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4_t*>(o + t * I + 4 * q) =
+                float4_t{acc[j][t][4 * q], acc[j][t][4 * q + 1], acc[j][t][4 * q + 2], acc[j][t][4 * q + 3]};
+      }
+    }
+    return;
+  }
+
   // SwiGLU: a lane's 16 hidden values of a row, the row's maximum over the 128
   // columns (the row's other lane, then the four waves), the codes
 #pragma unroll
@@ -240,8 +259,8 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
         codes[q] = none ? 0u
                         : e4m3x4_encode_nan(acc[j][0][4 * q] * inv, acc[j][0][4 * q + 1] * inv, acc[j][0][4 * q + 2] * inv,
                                             acc[j][0][4 * q + 3] * inv);
-      *reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(a.out) + (size_t)i * I + at.col * 128 + wn * 32 + h * 16) = codes;
-      if (wn == 0 && h == 0) a.outs[(size_t)i * (I / 128) + at.col] = scale;
+      *reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(a.out) + (size_t)i * I + tile_col * 128 + wn * 32 + h * 16) = codes;
+      if (wn == 0 && h == 0) a.outs[(size_t)i * (I / 128) + tile_col] = scale;
     }
   }
 }
@@ -270,7 +289,7 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_swiglu_kernel(GroupedArgs
 }  // namespace
 
 void launch_grouped_swiglu(bool mx, GroupedArgs a, hipStream_t stream) {
-  a.col_tiles = a.N / 256;
+  a.col_tiles = a.N / 256 * a.splits;
   const auto kernel = mx ? grouped_swiglu_kernel<true> : grouped_swiglu_kernel<false>;
   hipLaunchKernelGGL(kernel, dim3(grouped_workgroups(a, a.R, kRows)), dim3(kThreads), 0, stream, a);
 }

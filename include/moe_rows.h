@@ -17,8 +17,8 @@
  * one to three kernels on `stream` (a hipStream_t of the current device; NULL
  * is the default stream), allocates nothing, never synchronises, issues no
  * memset and keeps nothing between calls: it can be captured into a HIP graph
- * and calls on different streams are independent (each moe_route_rows call in
- * flight needs its own workspace).
+ * and calls on different streams are independent (each call in flight needs
+ * its own workspace).
  *
  * All pointers are device pointers, arrays row-major and contiguous; outputs
  * overlap no input (but for residual_out, below) and no other output. Nothing
@@ -168,6 +168,12 @@ size_t moe_route_rows_workspace(int32_t T, int32_t local_experts);
  *   products are exact and their sums FP32 throughout, and act is multiplied
  *   by the reciprocal of its scale, so a code next to a rounding border may
  *   differ from moe_decode_run's.
+ * workspace: NULL, or 16-byte aligned device memory of at least
+ *   moe_grouped_gemm_workspace / moe_grouped_swiglu_workspace bytes, with which
+ *   small calls are split over K and take up to a fourth of the time (SCRATCH_TOO_SMALL
+ *   where it is shorter). Its contents need no preparation and mean nothing
+ *   after the call; calls in flight at once need one each. Parts of K are
+ *   added in FP32, in order; their number depends on R, E, N and K alone.
  * K and N multiples of 128 (N of 256 for the SwiGLU), at most
  * MOE_ROWS_MAX_DIM; E <= 1024; X, R >= 0, at most 2^23 - 9 tiles of work
  * (floor(R/128) + E rows of ceil(N/256) tiles). FP8 and output arrays 16-byte aligned, E8M0
@@ -185,9 +191,16 @@ typedef struct moe_grouped_args {
   const float* w_scale;
   void* out;
   float* out_scale;  /* moe_grouped_swiglu */
+  void* workspace;
+  size_t workspace_bytes;
 } moe_grouped_args;
 int moe_grouped_gemm(const moe_grouped_args* a, void* stream);
 int moe_grouped_swiglu(const moe_grouped_args* a, void* stream);
+
+/* Bytes of workspace with which a call of these sizes splits K over workgroups
+ * (few rows or few columns; 0 where it would not). */
+size_t moe_grouped_gemm_workspace(int32_t R, int32_t E, int32_t N, int32_t K);
+size_t moe_grouped_swiglu_workspace(int32_t R, int32_t E, int32_t N, int32_t K);
 
 #ifdef __cplusplus
 }

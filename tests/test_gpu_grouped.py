@@ -234,6 +234,78 @@ def test_rows_behind_the_last_stay(counts):
     assert (h[n:] == 9).all() and (s[n:] == 5.0).all()
 
 
+def parts(d, glu):
+    """Parts of K that the call's workspace is for (1: none)."""
+    from fp8_block_scaled_moe_amd import lib
+
+    R = d["x"].shape[0] if d["rows"] is None else d["rows"].shape[0]
+    E, N, K = d["w"].shape
+    f = lib().moe_grouped_swiglu_workspace if glu else lib().moe_grouped_gemm_workspace
+    return max(1, f(R, E, N, K) // (R * N * 4))
+
+
+# few and ragged rows, with a K that is split unevenly
+@pytest.mark.parametrize("quant", ["fp8", "mxfp8"])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0, 5], RAGGED, [150, 0, 300]], ids=["one", "few", "ragged", "many"])
+def test_split_over_k(counts, gather, quant):
+    d = make(counts, 256, 128 * 37, 29, quant, gather)
+    assert parts(d, False) > 1 and parts(d, True) > 1
+    n = sum(counts)
+    y, (h, s) = check_gemm(d), check_swiglu(d)
+    again, (h2, s2) = call_gemm(d), grouped_swiglu(d["x"], d["x_scale"], d["w"], d["w_scale"], d["offsets"], limit=LIMIT, rows=d["rows"])
+    assert torch.equal(y[:n], again[:n]) and torch.equal(h[:n], h2[:n]) and torch.equal(s[:n], s2[:n])
+
+
+@pytest.mark.parametrize("K", [1024, 1152, 16384])
+def test_split_sizes(K):
+    """The shortest split K, one block more, a long one; an odd tile of columns."""
+    d = make([2, 0, 1, 30], 384, K, 30)
+    assert parts(d, False) > 1
+    check_gemm(d)
+    d = make([2, 0, 1, 30], 768, K, 31)
+    assert parts(d, True) > 1
+    check_swiglu(d)
+
+
+def test_split_leaves_other_rows_alone():
+    """With a workspace, as without: rows behind the last and before the first
+    group stay, rows with an index out of range are zeros, a NaN stays in its
+    row; a workspace past the need is not written behind it."""
+    import ctypes
+    from fp8_block_scaled_moe_amd import _rows, lib
+
+    d = make([7, 40], 256, 2048, 32, gather=True, extra=9)
+    d["rows"][5], d["rows"][20] = -1, 2**30
+    d["x"].view(torch.uint8)[int(d["rows"][11]), 1500] = 0x7F
+    d["offsets"][0] = 2
+    R, L, st = d["rows"].shape[0], lib(), torch.cuda.current_stream().cuda_stream
+    nan = (d["rows"] == d["rows"][11])[2:47]
+    zero = torch.zeros(45, dtype=torch.bool, device=DEV)
+    zero[[3, 18]] = True
+    ptrs = (d["x"].data_ptr(), d["x_scale"].data_ptr(), d["rows"].data_ptr(), d["offsets"].data_ptr(), d["w"].data_ptr(),
+            d["w_scale"].data_ptr())
+    for glu in (False, True):
+        need = (L.moe_grouped_swiglu_workspace if glu else L.moe_grouped_gemm_workspace)(R, 2, 256, 2048)
+        assert need > 0
+        ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+        out = torch.full((R, 128 if glu else 512), 9, dtype=torch.uint8, device=DEV)
+        s = torch.full((R, 1), 5.0, device=DEV)
+        a = _rows.GroupedArgs(R, d["x"].shape[0], 2, 256, 2048, 1, LIMIT, *ptrs, out.data_ptr(), s.data_ptr(), ws.data_ptr(), need)
+        assert (L.moe_grouped_swiglu if glu else L.moe_grouped_gemm)(ctypes.byref(a), st) == 0
+        torch.cuda.synchronize()
+        assert (ws[need:] == 0x5A).all()
+        for t, was in ((out, 9), (s, 5.0)):
+            assert (t[:2] == was).all() and (t[47:] == was).all()
+        rows = out[2:47]
+        assert not rows[zero].any()
+        if glu:
+            assert ((rows[nan] & 0x7F) == 0x7F).all() and not ((rows[~nan] & 0x7F) == 0x7F).any()
+        else:
+            y = out.view(torch.bfloat16)[2:47]
+            assert torch.isnan(y[nan]).all() and not torch.isnan(y[~nan]).any()
+
+
 @pytest.mark.parametrize("counts", [[4, 2], [40, 30], [300, 200]], ids=["few", "some", "many"])
 def test_rows_outside_give_zeros(counts):
     d = make(counts, 256, 256, 14, gather=True, extra=0)

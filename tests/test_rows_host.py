@@ -131,6 +131,24 @@ def test_grouped_own_errors(L):
     assert L.moe_grouped_swiglu(fill(_rows.GroupedArgs, GROUPED, dict(out_scale=None)), None) == INVALID
 
 
+def test_grouped_workspace(L):
+    """Something where K can be split over workgroups, nothing where the tiles
+    fill the GPU or K is short; too little of it and a misaligned one are
+    errors, none at all is not."""
+    need = L.moe_grouped_gemm_workspace(4, 2, 256, 4096)
+    assert need and need % (4 * 256 * 4) == 0
+    assert L.moe_grouped_swiglu_workspace(4, 2, 256, 4096)
+    for f in (L.moe_grouped_gemm_workspace, L.moe_grouped_swiglu_workspace):
+        assert f(4, 2, 256, 896) == 0 and f(100000, 256, 4096, 4096) == 0
+        assert f(0, 2, 256, 4096) == f(4, 0, 256, 4096) == f(4, 2, 0, 4096) == f(4, 2, 256, 0) == f(-1, 2, 256, 4096) == 0
+        # never more than one part for each of 256 CUs
+        for R in (1, 3, 100, 5000, 32768):
+            assert f(R, 8, 512, 8192) <= 256 * 256 * 256 * 4
+    for call in (L.moe_grouped_gemm, L.moe_grouped_swiglu):
+        for over, code in ((dict(workspace=P, workspace_bytes=need - 1), SMALL), (dict(workspace=P + 8, workspace_bytes=need), INVALID)):
+            assert call(fill(_rows.GroupedArgs, GROUPED, dict(K=4096, **over)), None) == code
+
+
 def test_null_argument_blocks(L):
     for f in (L.moe_add_rmsnorm_quant, L.moe_route_rows, L.moe_grouped_gemm, L.moe_grouped_swiglu):
         assert f(None, None) == INVALID
