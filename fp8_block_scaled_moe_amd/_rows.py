@@ -2,9 +2,10 @@
 tokens, as separate calls.
 
 Argument checks and marshalling only. Every call allocates its outputs (and
-route_rows and the grouped products their workspace) from torch's caching allocator and launches on the
-current stream of the tensors' device, or on `stream` when one is given; it
-never synchronises, so it can be captured into a graph.
+all but the norm a workspace where one is needed) from torch's caching
+allocator and launches on the current stream of the tensors' device, or on
+`stream` when one is given; it never synchronises, so it can be captured into
+a graph.
 """
 
 from __future__ import annotations

@@ -24,11 +24,12 @@ struct GroupedArgs {
 
 // Parts of K for so few tiles (of up to `rows` rows by 256 weight rows) that
 // they leave CUs idle: as many as give every CU a part, of four 128-wide blocks
-// and more. See grouped_gemm.hip.
+// and more, from 16 blocks on (below, the second launch costs what it saves). See
+// grouped_gemm.hip.
 inline int grouped_splits(int R, int E, int N, int K, int rows) {
   const int64_t full = (int64_t)R / rows + E, tiles = (full < R ? full : R) * ((N + 255) / 256);
   const int64_t most = K / 128 / 4, wanted = tiles > 0 ? 256 / tiles : 1;
-  return (int)(wanted < 2 || most < 2 ? 1 : wanted < most ? wanted : most);
+  return (int)(wanted < 2 || most < 4 ? 1 : wanted < most ? wanted : most);
 }
 
 // Workgroups that find_tile's tiles need at most for R grouped rows (each

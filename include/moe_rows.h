@@ -170,10 +170,11 @@ size_t moe_route_rows_workspace(int32_t T, int32_t local_experts);
  *   differ from moe_decode_run's.
  * workspace: NULL, or 16-byte aligned device memory of at least
  *   moe_grouped_gemm_workspace / moe_grouped_swiglu_workspace bytes, with which
- *   small calls are split over K and take up to a fourth of the time (SCRATCH_TOO_SMALL
+ *   small calls are split over K, up to 3.7 times faster (SCRATCH_TOO_SMALL
  *   where it is shorter). Its contents need no preparation and mean nothing
  *   after the call; calls in flight at once need one each. Parts of K are
- *   added in FP32, in order; their number depends on R, E, N and K alone.
+ *   added in FP32, in order; their number depends on R, E, N and K alone, so
+ *   a row's last FP32 bits may differ between calls of different R.
  * K and N multiples of 128 (N of 256 for the SwiGLU), at most
  * MOE_ROWS_MAX_DIM; E <= 1024; X, R >= 0, at most 2^23 - 9 tiles of work
  * (floor(R/128) + E rows of ceil(N/256) tiles). FP8 and output arrays 16-byte aligned, E8M0

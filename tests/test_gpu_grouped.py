@@ -257,7 +257,7 @@ def test_split_over_k(counts, gather, quant):
     assert torch.equal(y[:n], again[:n]) and torch.equal(h[:n], h2[:n]) and torch.equal(s[:n], s2[:n])
 
 
-@pytest.mark.parametrize("K", [1024, 1152, 16384])
+@pytest.mark.parametrize("K", [2048, 2176, 16384])
 def test_split_sizes(K):
     """The shortest split K, one block more, a long one; an odd tile of columns."""
     d = make([2, 0, 1, 30], 384, K, 30)

@@ -139,7 +139,7 @@ def test_grouped_workspace(L):
     assert need and need % (4 * 256 * 4) == 0
     assert L.moe_grouped_swiglu_workspace(4, 2, 256, 4096)
     for f in (L.moe_grouped_gemm_workspace, L.moe_grouped_swiglu_workspace):
-        assert f(4, 2, 256, 896) == 0 and f(100000, 256, 4096, 4096) == 0
+        assert f(4, 2, 256, 1920) == 0 and f(100000, 256, 4096, 4096) == 0
         assert f(0, 2, 256, 4096) == f(4, 0, 256, 4096) == f(4, 2, 0, 4096) == f(4, 2, 256, 0) == f(-1, 2, 256, 4096) == 0
         # never more than one part for each of 256 CUs
         for R in (1, 3, 100, 5000, 32768):
