@@ -268,6 +268,41 @@ def test_split_sizes(K):
     check_swiglu(d)
 
 
+def test_split_calls_captured_and_at_once():
+    """Split calls in two graphs and on two streams: each replay, with eager
+    calls and new inputs between them, equals the eager result."""
+    ds = [make([3, 0, 17], 256, 2048, 33 + i, extra=0) for i in range(2)]
+    both = lambda d: (call_gemm(d), *grouped_swiglu(d["x"], d["x_scale"], d["w"], d["w_scale"], d["offsets"], limit=LIMIT))  # noqa: E731
+    assert all(parts(d, glu) > 1 for d in ds for glu in (False, True))
+    for d in ds:
+        both(d)
+    torch.cuda.synchronize()
+    graphs = []
+    for d in ds:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = both(d)
+        graphs.append((g, out))
+    streams = [torch.cuda.Stream() for _ in ds]
+    gen = torch.Generator(device=DEV).manual_seed(35)
+    for _ in range(4):
+        for d in ds:
+            d["x"].copy_(codes(gen, d["x"].shape, 100.0))
+        want = [both(d) for d in ds]
+        torch.cuda.synchronize()
+        for (g, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        eager = []
+        for d, st in zip(ds, streams):
+            with torch.cuda.stream(st):
+                eager.append(both(d))
+        torch.cuda.synchronize()
+        for w, e, (_, o) in zip(want, eager, graphs):
+            assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(w, e, o))
+
+
 def test_split_leaves_other_rows_alone():
     """With a workspace, as without: rows behind the last and before the first
     group stay, rows with an index out of range are zeros, a NaN stays in its
