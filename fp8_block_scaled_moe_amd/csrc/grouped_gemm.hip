@@ -2,8 +2,9 @@
 // moe_grouped_gemm and moe_grouped_swiglu, over the kernels of
 // grouped_product.hip and grouped_swiglu.hip, and the joining of split sums.
 //
-// A tile's K blocks come one after the other, three at a time: about 0.8 us each,
-// whatever the number of tiles. Where the tiles leave CUs idle, K is split over
+// A tile's K blocks come one after the other: 0.7 us and more each, whatever the
+// number of tiles, since a CU takes in some 60 GB/s by these copies (a fourth block
+// in LDS changes nothing). Where the tiles leave CUs idle, K is split over
 // workgroups, whose FP32 sums go to the workspace and are added here in
 // order (no atomics), before the rounding or the SwiGLU. Without and with it,
 // calls in a graph, one token's 6 experts with 512 columns: product, K = 1024, 8.5
