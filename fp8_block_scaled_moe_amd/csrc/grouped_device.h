@@ -59,8 +59,8 @@ struct TileAt {
 };
 
 // A workgroup's part of K, in 128-wide blocks, and the block of it that the
-// workgroup begins with (at() wraps round; code of its own, since the wrapping
-// costs the others 2%). Where K is a multiple of 4096, the
+// workgroup begins with (at() wraps round). A tile with all of K from its beginning
+// on (whole_k) has code of its own: the others' costs it 2%. Where K is a multiple of 4096, the
 // blocks of one index of all rows lie in few memory channels, so tiles with
 // weights of their own begin at different blocks. Product, 16 rows for each of
 // 32 experts, N = 2048, without and with it: K = 4096, 64.3 and 45.5 us; 8192, 118 and
@@ -68,12 +68,17 @@ struct TileAt {
 // weights (SwiGLU, 500 rows an expert, K = 8192: 1.17 and 1.20 ms) it costs.
 struct KPart {
   int split, first, blocks, start;
-  template <bool kTurned>
+  template <bool kWhole>
   __device__ __forceinline__ int at(int b) const {
-    return kTurned ? b + start - (b + start >= blocks ? blocks : 0) : b;
+    return kWhole ? b : b + start - (b + start >= blocks ? blocks : 0);
   }
 };
+__device__ __forceinline__ bool whole_k(const GroupedArgs& a, const TileAt& at) {
+  return a.splits == 1 && !(at.only && a.K % 4096 == 0);
+}
+template <bool kWhole>
 __device__ __forceinline__ KPart k_part(const GroupedArgs& a, const TileAt& at) {
+  if (kWhole) return KPart{0, 0, a.K / 128, 0};
   const int KB = a.K / 128, split = at.col % a.splits;
   const int lo = KB * split / a.splits, n = KB * (split + 1) / a.splits - lo;
   int start = 0;

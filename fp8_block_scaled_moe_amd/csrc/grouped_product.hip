@@ -73,15 +73,16 @@ __device__ __forceinline__ float4_t product(const int8v_t& w, const int8v_t& x, 
 }
 
 // kJ: the most 16-row groups of a wave; `first`: those of the first four waves.
-template <bool kMx, bool kTurned, int kJ>
-__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, const KPart& part, uint8_t* shared, int groups) {
+template <bool kMx, bool kWhole, int kJ>
+__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, uint8_t* shared, int groups) {
   Stage<kJ>* const sm = reinterpret_cast<Stage<kJ>*>(shared);
   constexpr int kHalf = kJ * kGroup;  // LDS rows of a half of the waves
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r16 = lane & 15, g = lane >> 4;
   const int wn = wave & 3, wm = wave >> 2;
-  const int first = (groups + 1) / 2, tile_col = at.col / a.splits;
+  const int first = (groups + 1) / 2, tile_col = kWhole ? at.col : at.col / a.splits;
+  const KPart part = k_part<kWhole>(a, at);
   const int KB = part.blocks;
 
   // What this wave copies of a block: 32 LDS rows of the weights, kRows / 8 of
@@ -117,7 +118,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, con
   const uint32_t lds = lds_offset(shared);
   constexpr int kWCopies = 4;
   const auto issue_w = [&](int st, int b) {
-    const int kb = part.at<kTurned>(b);
+    const int kb = part.at<kWhole>(b);
     const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kJ>);
     const size_t k0 = (size_t)kb * 128;
     const auto all = [&](auto once) {
@@ -132,7 +133,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, con
       all(std::false_type{});
   };
   const auto issue_x = [&](int st, int b) {
-    const int kb = part.at<kTurned>(b);
+    const int kb = part.at<kWhole>(b);
     const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kJ>);
 #pragma unroll
     for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + (size_t)kb * 128, to + (wx + i) * 1024);
@@ -194,7 +195,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, con
   load_x(0, 0);
   int st = 0;
   for (int b = 0; b < KB; ++b) {
-    const float s0 = sw[part.at<kTurned>(b)];
+    const float s0 = sw[part.at<kWhole>(b)];
     if (b + kStages<kJ> < KB) {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       workgroup_barrier();  // every wave has read the block's weights
@@ -235,7 +236,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, con
   for (int j = 0; j < kJ; ++j) {
     const int i = at.row + (wm * first + j) * kGroup + r16;
     if (j < (wm ? groups - first : first) && i < at.end) {
-      if (a.splits > 1) {
+      if (!kWhole && a.splits > 1) {
         float* o = a.partial + ((size_t)part.split * a.R + i) * a.N + n0 + g * 8;
 #pragma unroll
         for (int s = 0; s < 4; ++s) *reinterpret_cast<float4_t*>(o + 32 * (s >> 1) + 4 * (s & 1)) = acc[j][s];
@@ -254,20 +255,20 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, con
   }
 }
 
-template <bool kMx, bool kTurned>
-__device__ __forceinline__ void any_tile(const GroupedArgs& a, const TileAt& at, const KPart& part, uint8_t* shared) {
+template <bool kMx, bool kWhole>
+__device__ __forceinline__ void any_tile(const GroupedArgs& a, const TileAt& at, uint8_t* shared) {
   const int groups = (at.end - at.row + kGroup - 1) / kGroup;
   const int need = (groups + 1) / 2;  // of the first half of the waves; the other half has the rest
   if (need > 6)
-    tile<kMx, kTurned, 8>(a, at, part, shared, groups);
+    tile<kMx, kWhole, 8>(a, at, shared, groups);
   else if (need > 4)
-    tile<kMx, kTurned, 6>(a, at, part, shared, groups);
+    tile<kMx, kWhole, 6>(a, at, shared, groups);
   else if (need > 2)
-    tile<kMx, kTurned, 4>(a, at, part, shared, groups);
+    tile<kMx, kWhole, 4>(a, at, shared, groups);
   else if (need > 1)
-    tile<kMx, kTurned, 2>(a, at, part, shared, groups);
+    tile<kMx, kWhole, 2>(a, at, shared, groups);
   else
-    tile<kMx, kTurned, 1>(a, at, part, shared, groups);
+    tile<kMx, kWhole, 1>(a, at, shared, groups);
 }
 
 template <bool kMx>
@@ -275,11 +276,10 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_product_kernel(GroupedArg
   __shared__ alignas(16) uint8_t shared[kShared];
   const TileAt at = find_tile<kRows, kGroup, kThreads>(a, blockIdx.x);
   if (at.e < 0) return;
-  const KPart part = k_part(a, at);
-  if (part.start)
-    any_tile<kMx, true>(a, at, part, shared);
+  if (whole_k(a, at))
+    any_tile<kMx, true>(a, at, shared);
   else
-    any_tile<kMx, false>(a, at, part, shared);
+    any_tile<kMx, false>(a, at, shared);
 }
 
 }  // namespace

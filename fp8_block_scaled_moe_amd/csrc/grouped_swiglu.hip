@@ -61,8 +61,8 @@ __device__ __forceinline__ Wide16 widen16(const u32x4_t& q, float scale) {
 }
 
 // kJ: the 32-row groups of this wave; kFirst: those of the first four waves.
-template <bool kMx, bool kTurned, int kFirst, int kJ>
-__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, const KPart& part, Shared& sm) {
+template <bool kMx, bool kWhole, int kFirst, int kJ>
+__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared& sm) {
   constexpr int kHalf = kFirst * kGroup;  // LDS rows of a half of the waves
   const Stage<kFirst>* const stage = reinterpret_cast<const Stage<kFirst>*>(sm.st);
   constexpr int kN = kJ ? kJ : 1;
@@ -70,7 +70,8 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, con
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r32 = lane & 31, h = lane >> 5;
   const int wn = wave & 3, wm = wave >> 2;
-  const int I = a.N / 2, tile_col = at.col / a.splits;
+  const int I = a.N / 2, tile_col = kWhole ? at.col : at.col / a.splits;
+  const KPart part = k_part<kWhole>(a, at);
   const int KB = part.blocks;
 
   // What this wave copies of a block: 32 LDS rows of the weights, 16 of the
@@ -101,7 +102,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, con
   const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + (x_of(sl + lane) * (a.K / 128) + part.first) * 4;
   const uint32_t lds = lds_offset(sm.st);
   const auto issue = [&](int st, int b) {
-    const int kb = part.at<kTurned>(b);
+    const int kb = part.at<kWhole>(b);
     const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kFirst>);
     const size_t k0 = (size_t)kb * 128;
     const auto weights = [&](auto once) {
@@ -182,7 +183,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, con
   load(0, 0);
   int st = 0;
   for (int b = 0; b < KB; ++b) {
-    const float s0 = su[part.at<kTurned>(b)], s1 = sg[part.at<kTurned>(b)];
+    const float s0 = su[part.at<kWhole>(b)], s1 = sg[part.at<kWhole>(b)];
     load(st, 1);
     multiply(0);
     load(st, 2);
@@ -211,7 +212,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, con
         for (int i = 0; i < 16; ++i) acc[j][t][i] = fmaf(p[j][t][i], sc[j][t], acc[j][t][i]);
   }
 
-  if (a.splits > 1) {
+  if (!kWhole && a.splits > 1) {
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
       const int i = at.row + (wm * kFirst + j) * kGroup + r32;
@@ -265,21 +266,21 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, con
   }
 }
 
-template <bool kMx, bool kTurned>
-__device__ __forceinline__ void any_tile(const GroupedArgs& a, const TileAt& at, const KPart& part, Shared& sm) {
+template <bool kMx, bool kWhole>
+__device__ __forceinline__ void any_tile(const GroupedArgs& a, const TileAt& at, Shared& sm) {
   // the first half of the waves takes half of the 32-row groups, rounded up,
   // the other the rest; all branches meet the same barriers
   const int groups = (at.end - at.row + kGroup - 1) / kGroup, first = (groups + 1) / 2;
   const bool half = threadIdx.x < kThreads / 2;
   if (first == 2) {
     if (half || groups == 4)
-      tile<kMx, kTurned, 2, 2>(a, at, part, sm);
+      tile<kMx, kWhole, 2, 2>(a, at, sm);
     else
-      tile<kMx, kTurned, 2, 1>(a, at, part, sm);
+      tile<kMx, kWhole, 2, 1>(a, at, sm);
   } else if (half || groups == 2) {
-    tile<kMx, kTurned, 1, 1>(a, at, part, sm);
+    tile<kMx, kWhole, 1, 1>(a, at, sm);
   } else {
-    tile<kMx, kTurned, 1, 0>(a, at, part, sm);
+    tile<kMx, kWhole, 1, 0>(a, at, sm);
   }
 }
 
@@ -288,11 +289,10 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_swiglu_kernel(GroupedArgs
   __shared__ Shared sm;
   const TileAt at = find_tile<kRows, kGroup, kThreads>(a, blockIdx.x);
   if (at.e < 0) return;
-  const KPart part = k_part(a, at);
-  if (part.start)
-    any_tile<kMx, true>(a, at, part, sm);
+  if (whole_k(a, at))
+    any_tile<kMx, true>(a, at, sm);
   else
-    any_tile<kMx, false>(a, at, part, sm);
+    any_tile<kMx, false>(a, at, sm);
 }
 
 }  // namespace

@@ -268,6 +268,19 @@ def test_split_sizes(K):
     check_swiglu(d)
 
 
+def test_long_k_turned():
+    """K = 4096, enough tiles not to be split: tiles of an expert with one row
+    tile begin at blocks of their own, others at the first, with the same sums."""
+    counts = [(7 * e) % 23 for e in range(38)] + [140, 300]
+    d = make(counts, 1024, 4096, 36, gather=True)
+    assert parts(d, False) == parts(d, True) == 1
+    check_gemm(d)
+    h, s = check_swiglu(d)
+    again = grouped_swiglu(d["x"], d["x_scale"], d["w"], d["w_scale"], d["offsets"], limit=LIMIT, rows=d["rows"])
+    n = sum(counts)
+    assert torch.equal(h[:n], again[0][:n]) and torch.equal(s[:n], again[1][:n])
+
+
 def test_split_calls_captured_and_at_once():
     """Split calls in two graphs and on two streams: each replay, with eager
     calls and new inputs between them, equals the eager result."""
