@@ -7,9 +7,9 @@
 // expert, a 64-bit mask of the tokens that picked it (LDS or-atomics: the
 // same mask in any order), and a route's place is
 //   offset of the expert + count of earlier chunks + tokens below in the mask.
-// Up to 32 tokens one workgroup does all of it (one launch). Beyond, three:
-// picks and counts per (chunk, expert), the running sums over the chunks,
-// and the places. The bound is instructions, not memory: 16,384 tokens x 256
+// Up to 32 tokens one workgroup does all of it (one launch). Beyond, two or
+// three: picks and counts per (chunk, expert), the running sums over the chunks
+// where there are many, and the places. The bound is instructions, not memory: 16,384 tokens x 256
 // experts are 16 MB of logits (4 us), but some 370 vector instructions a token,
 // 12 of the first launch's 18 us; the other two take 4.7 and 4.3 us. One token:
 // 4.5 us, all of it latency.
@@ -24,7 +24,7 @@ namespace moe {
 namespace {
 
 // Most tokens of the single workgroup: 32 tokens x 256 experts take it 9.7 us,
-// 64 16.3, where the three launches take 11.9 (in a graph, from 33 tokens on).
+// 64 16.3, where two launches take 9.7 (in a graph).
 constexpr int kOneLaunch = 32;
 constexpr int kMaxChunk = 64;  // tokens of a workgroup: a mask's bits
 constexpr int kRouteThreads = 1024;
@@ -32,6 +32,11 @@ constexpr int kRouteWaves = kRouteThreads / kWave;
 constexpr int kScanExperts = 16;  // experts per workgroup of the chunk sums
 constexpr int kScanBatch = 4;     // counts requested before they are added
 constexpr int kScanParts = kRouteThreads / kScanExperts;
+// Chunks whose counts every workgroup of the last launch sums by itself: without
+// the launch between, 128 tokens x 256 experts take 9.9 us and not 12.0, 512 11.6
+// and 12.5; with 64 chunks (1,024 tokens) 13.6 and 12.7.
+constexpr int kFewChunks = 32;
+constexpr int kCountBatch = 16;  // counts that it requests at a time
 
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
 
@@ -329,7 +334,25 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(moe_route_ar
   const int* ws = static_cast<const int*>(a.workspace);
   const int e = threadIdx.x;
   const bool live = e < a.local_experts;
-  const int all = live ? ws[e] : 0, before = live ? ws[a.local_experts + (size_t)blockIdx.x * a.local_experts + e] : 0;
+  const int chunks = gridDim.x;
+  const int* count = ws + a.local_experts + (live ? e : 0);
+  int all = 0, before = 0;
+  if (chunks <= kFewChunks) {  // counts as the first launch left them
+    for (int c = 0; c < chunks; c += kCountBatch) {
+      int v[kCountBatch];
+#pragma unroll
+      for (int q = 0; q < kCountBatch; ++q) v[q] = count[(size_t)min(c + q, chunks - 1) * a.local_experts];
+#pragma unroll
+      for (int q = 0; q < kCountBatch; ++q) {
+        all += c + q < chunks ? v[q] : 0;
+        before += c + q < (int)blockIdx.x ? v[q] : 0;
+      }
+    }
+    if (!live) all = before = 0;
+  } else if (live) {
+    all = ws[e];
+    before = count[(size_t)blockIdx.x * a.local_experts];
+  }
   int total;
   const int first = block_exclusive(all, sm.wave_sum, total);
   if (live) sm.base[e] = first + before;
@@ -349,7 +372,8 @@ void launch_route(const moe_route_args& a, hipStream_t stream) {
   }
   const int chunk = chunk_tokens(a.T), chunks = (a.T + chunk - 1) / chunk;
   hipLaunchKernelGGL(route_pick_kernel<kPer>, dim3(chunks), dim3(kRouteThreads), 0, stream, a);
-  hipLaunchKernelGGL(route_sum_kernel, dim3((a.local_experts + kScanExperts - 1) / kScanExperts), dim3(kRouteThreads), 0,
+  if (chunks > kFewChunks)
+    hipLaunchKernelGGL(route_sum_kernel, dim3((a.local_experts + kScanExperts - 1) / kScanExperts), dim3(kRouteThreads), 0,
                      stream, static_cast<int*>(a.workspace), chunks, a.local_experts);
   hipLaunchKernelGGL(route_place_kernel, dim3(chunks), dim3(kRouteThreads), 0, stream, a);
 }
