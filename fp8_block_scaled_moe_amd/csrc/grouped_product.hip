@@ -85,8 +85,8 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, uin
   const KPart part = k_part<kWhole>(a, at);
   const int KB = part.blocks;
 
-  // What this wave copies of a block: 32 LDS rows of the weights, kRows / 8 of
-  // the activations, 64 scales (the same ones by several waves, so that every
+  // What this wave copies of a block: 32 LDS rows of the weights, 4 kJ of the
+  // activations (8 for kJ = 1, the same ones by two waves), 64 scales (the same ones by several waves, so that every
   // wave has as many copies on its way). LDS row L keeps 16-byte chunk c of
   // its row at place c ^ (L / 2 % 8), so that the 16 rows of a read phase
   // differ in bank. A lane's results of instructions s = 0, 1 (2, 3) of a

@@ -74,9 +74,9 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const KPart part = k_part<kWhole>(a, at);
   const int KB = part.blocks;
 
-  // What this wave copies of a block: 32 LDS rows of the weights, 16 of the
-  // activations and 64 scales (the same ones by four waves each, so that every
-  // wave has as many copies on its way). LDS row L keeps 16-byte chunk c of its
+  // What this wave copies of a block: 32 LDS rows of the weights, 8 kFirst
+  // of the activations and 64 scales (the same ones by several waves, so that
+  // every wave has as many copies on its way). LDS row L keeps 16-byte chunk c of its
   // row at place c ^ (L / 2 % 8), so that the 16 rows of a read phase differ in
   // bank. A wave's results of an instruction are weight rows 8 a + 4 h + b (a,
   // b = 0..3) of its 32: these are columns 16 h + 4 a + b, so that a lane's 16

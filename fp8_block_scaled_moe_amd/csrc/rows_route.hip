@@ -9,10 +9,10 @@
 //   offset of the expert + count of earlier chunks + tokens below in the mask.
 // Up to 32 tokens one workgroup does all of it (one launch). Beyond, two or
 // three: picks and counts per (chunk, expert), the running sums over the chunks
-// where there are many, and the places. The bound is instructions, not memory: 16,384 tokens x 256
-// experts are 16 MB of logits (4 us), but some 370 vector instructions a token,
-// 12 of the first launch's 18 us; the other two take 4.7 and 4.3 us. One token:
-// 4.5 us, all of it latency.
+// where there are many, and the places. The bound is instructions, not memory:
+// 16,384 tokens x 256 experts are 16 MB of logits (4 us), but some 370 vector
+// instructions a token, 12 of the first launch's 18 us; the other two take 4.7
+// and 4.3 us. One token: 4.5 us, all of it latency.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

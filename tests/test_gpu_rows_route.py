@@ -45,7 +45,7 @@ def check(logits, bias, k, scale=2.5, **local):
 
 
 # tokens around the one-workgroup form (32) and the ends of chunks; experts around each number per lane
-@pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200])
+@pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200, 512, 513])
 @pytest.mark.parametrize("E,k", [(8, 2), (256, 8)])
 def test_tokens(T, E, k):
     check(*make(T, E, T + E), k)
