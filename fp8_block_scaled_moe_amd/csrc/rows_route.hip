@@ -364,6 +364,12 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(moe_route_ar
   place_routes(a, t0, n, sm.picks, sm.mask, sm.base);
 }
 
+// No tokens: zero offsets, and nothing else is read or written (the other
+// pointers may be NULL then).
+__global__ __launch_bounds__(kRouteThreads) void route_none_kernel(int* offsets, int n) {
+  for (int e = threadIdx.x; e < n; e += kRouteThreads) offsets[e] = 0;
+}
+
 template <int kPer>
 void launch_route(const moe_route_args& a, hipStream_t stream) {
   if (a.T <= kOneLaunch) {
@@ -414,7 +420,9 @@ int moe_route_rows(const moe_route_args* args, void* stream) {
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int per = (a.E + kWave - 1) / kWave;
-  if (per <= 1)
+  if (a.T == 0)
+    hipLaunchKernelGGL(route_none_kernel, dim3(1), dim3(kRouteThreads), 0, s, a.offsets, a.local_experts + 1);
+  else if (per <= 1)
     launch_route<1>(a, s);
   else if (per <= 2)
     launch_route<2>(a, s);

@@ -117,7 +117,8 @@ int moe_add_rmsnorm_quant(const moe_norm_args* a, void* stream);
  *           preparation and mean nothing after the call. May be NULL when
  *           that size is 0.
  * 1 <= k <= min(E, 32), E <= 1024, 0 <= T <= MOE_ROWS_MAX_TOKENS,
- * routed_scale finite, local_experts >= 1 within [0, E). T = 0 writes zero offsets. */
+ * routed_scale finite, local_experts >= 1 within [0, E). T = 0 writes zero
+ * offsets and touches nothing else: every other pointer may be NULL then. */
 typedef struct moe_route_args {
   int32_t T, E, k;
   int32_t logits_dtype; /* MOE_DTYPE_F32 or MOE_DTYPE_BF16 */

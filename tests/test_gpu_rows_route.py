@@ -129,6 +129,18 @@ def test_no_tokens():
     assert r.ids.shape == (0, 2) and r.rows.shape == (0,) and r.offsets.tolist() == [0] * 17
 
 
+@pytest.mark.parametrize("E,lb,lc", [(1, 0, 1), (16, 4, 8), (1024, 0, 1024)])
+def test_no_tokens_needs_the_offsets_alone(E, lb, lc):
+    """An empty batch of a C caller: every pointer but offsets is NULL."""
+    import ctypes
+    from fp8_block_scaled_moe_amd import _rows, lib
+
+    buf = torch.full((lc + 3,), -7, dtype=torch.int32, device=DEV)
+    a = _rows.RouteArgs(T=0, E=E, k=1, local_begin=lb, local_experts=lc, routed_scale=1.0, offsets=buf[1:].data_ptr())
+    assert lib().moe_route_rows(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    assert buf.tolist() == [-7] + [0] * (lc + 1) + [-7]
+
+
 def test_rows_behind_the_last_stay(T=100):
     """Entries of rows from offsets[-1] on are not written."""
     import ctypes
