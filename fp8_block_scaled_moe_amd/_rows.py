@@ -19,6 +19,7 @@ import torch
 from ._capi import DTYPE_BF16, DTYPE_F32, MoeDecodeError, OK, _FP8, _need, lib
 
 QUANT = {None: 0, "fp8": 1, "fp8_p2": 2, "mxfp8": 3}
+SUMS = {"fp32": 0, "fp8": 1}
 ROWS_MAX_D = 16384
 ROWS_MAX_TOKENS = 1048576
 _I32_MAX = 2**31 - 1  # sizes are 32-bit integers in the C ABI
@@ -47,7 +48,7 @@ class GroupedArgs(ctypes.Structure):
     _fields_ = [("R", _i32), ("X", _i32), ("E", _i32), ("N", _i32), ("K", _i32), ("quant", _i32),
                 ("limit", _f32), ("x", _vp), ("x_scale", _vp), ("rows", _vp),
                 ("offsets", _vp), ("w", _vp), ("w_scale", _vp), ("out", _vp), ("out_scale", _vp), ("workspace", _vp),
-                ("workspace_bytes", ctypes.c_size_t)]
+                ("workspace_bytes", ctypes.c_size_t), ("sums", _i32)]
 
 
 class RoutedRows(NamedTuple):
@@ -260,7 +261,7 @@ def _grouped(x, x_scale, w, w_scale, offsets, rows):
 
 
 def grouped_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, offsets: torch.Tensor,
-                 *, rows: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                 *, rows: Optional[torch.Tensor] = None, sums: str = "fp32", stream=None) -> torch.Tensor:
     """[R, N] BF16 product of every expert with its own rows (include/moe_rows.h):
     grouped row i of expert e (offsets[e] <= i < offsets[e + 1]) is
     x[rows[i]] (x[i] without rows) times w[e]^T.
@@ -268,7 +269,10 @@ def grouped_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scal
     x [X, K] e4m3 codes (uint8 or float8_e4m3fn) with x_scale [X, K/128] FP32
     or, for MXFP8, [X, K/32] E8M0 bytes (uint8 or float8_e8m0fnu); w [E, N, K]
     e4m3 with w_scale [E, N/128, K/128] FP32. Rows from offsets[E] on are left
-    unwritten."""
+    unwritten. sums: "fp32", or "fp8" for the faster and coarser ones of the
+    FP8 matrix instruction."""
+    if sums not in SUMS:
+        raise ValueError(f"sums must be one of {list(SUMS)}, got {sums!r}")
     dev, R, sizes, ptrs = _grouped(x, x_scale, w, w_scale, offsets, rows)
     with _where(dev, stream):
         out = torch.empty((R, sizes[3]), dtype=torch.bfloat16, device=dev)
@@ -276,7 +280,7 @@ def grouped_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scal
             need = lib().moe_grouped_gemm_workspace(R, *sizes[2:5])
             ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
             _call("moe_grouped_gemm", GroupedArgs(*sizes, 0.0, *ptrs, out.data_ptr(), None,
-                                                  None if ws is None else ws.data_ptr(), need), dev)
+                                                  None if ws is None else ws.data_ptr(), need, SUMS[sums]), dev)
     return out
 
 

@@ -22,12 +22,14 @@ struct GroupedArgs {
   int col_tiles;   // column tiles of an expert's output times `splits`
 };
 
-// Parts of K for so few tiles (of up to `rows` rows by 256 weight rows) that
+constexpr int kTileRows = 128;  // of a tile with FP32 sums, at most
+
+// Parts of K for so few tiles (of up to 128 rows by 256 weight rows) that
 // they leave CUs idle: as many as give every CU a part, of four 128-wide blocks
 // and more, from 16 blocks on (below, the second launch costs what it saves). See
 // grouped_gemm.hip.
-inline int grouped_splits(int R, int E, int N, int K, int rows) {
-  const int64_t full = (int64_t)R / rows + E, tiles = (full < R ? full : R) * ((N + 255) / 256);
+inline int grouped_splits(int R, int E, int N, int K) {
+  const int64_t full = (int64_t)R / kTileRows + E, tiles = (full < R ? full : R) * ((N + 255) / 256);
   const int64_t most = K / 128 / 4, wanted = tiles > 0 ? 256 / tiles : 1;
   return (int)(wanted < 2 || most < 4 ? 1 : wanted < most ? wanted : most);
 }
@@ -46,9 +48,9 @@ typedef const __attribute__((address_space(4))) int32_t* uniform_ints;
 __device__ __forceinline__ uniform_floats as_uniform(const float* p) { return (uniform_floats)(uintptr_t)p; }
 __device__ __forceinline__ uniform_ints as_uniform(const int32_t* p) { return (uniform_ints)(uintptr_t)p; }
 
-constexpr int kProductRows = 256, kSwigluRows = 128;                      // of a tile, at most
-void launch_grouped_product(bool mx, GroupedArgs a, hipStream_t stream);  // grouped_product.hip
-void launch_grouped_swiglu(bool mx, GroupedArgs a, hipStream_t stream);   // grouped_swiglu.hip
+void launch_grouped_product(bool mx, GroupedArgs a, hipStream_t stream);      // grouped_product.hip
+void launch_grouped_product_fp8(bool mx, GroupedArgs a, hipStream_t stream);  // grouped_product_fp8.hip
+void launch_grouped_swiglu(bool mx, GroupedArgs a, hipStream_t stream);       // grouped_swiglu.hip
 
 // A workgroup's tile: grouped rows [row, end) of expert e, column tile and
 // part of K `col`;

@@ -1,6 +1,7 @@
 // Products grouped by expert over ragged rows (include/moe_rows.h): the calls
 // moe_grouped_gemm and moe_grouped_swiglu, over the kernels of
-// grouped_product.hip and grouped_swiglu.hip, and the joining of split sums.
+// grouped_product.hip, grouped_product_fp8.hip and grouped_swiglu.hip, and the
+// joining of split sums.
 //
 // A tile's K blocks come one after the other: 0.7 us and more each, whatever the
 // number of tiles, since a CU takes in some 60 GB/s by these copies (a fourth block
@@ -88,9 +89,9 @@ void launch_join(void (*kernel)(GroupedArgs), const GroupedArgs& a, int64_t colu
   hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kJoinThreads), 0, stream, a);
 }
 
-size_t workspace(int R, int E, int N, int K, int rows) {
+size_t workspace(int R, int E, int N, int K) {
   if (R <= 0 || E <= 0 || N <= 0 || K <= 0) return 0;
-  const int splits = grouped_splits(R, E, N, K, rows);
+  const int splits = grouped_splits(R, E, N, K);
   return splits > 1 ? (size_t)splits * R * N * sizeof(float) : 0;
 }
 
@@ -101,7 +102,7 @@ int check(const moe_grouped_args* p) {
   const moe_grouped_args& a = *p;
   if (a.R < 0 || a.X < 0 || a.E < 1 || a.N < 1 || a.K < 1) return MOE_DECODE_ERR_INVALID_ARG;
   if (a.E > MOE_DECODE_MAX_EXPERTS || a.N % 128 || a.K % 128 || a.N > MOE_ROWS_MAX_DIM || a.K > MOE_ROWS_MAX_DIM ||
-      a.quant < MOE_QUANT_FP8 || a.quant > MOE_QUANT_MXFP8)
+      a.quant < MOE_QUANT_FP8 || a.quant > MOE_QUANT_MXFP8 || a.sums < MOE_SUMS_FP32 || a.sums > MOE_SUMS_FP8)
     return MOE_DECODE_ERR_UNSUPPORTED;
   if (a.R == 0) return MOE_DECODE_OK;
   if (a.X < (a.rows ? 1 : a.R)) return MOE_DECODE_ERR_INVALID_ARG;
@@ -121,7 +122,7 @@ int check_workspace(const moe_grouped_args& a, size_t need) {
   return a.workspace_bytes < need ? MOE_DECODE_ERR_SCRATCH_TOO_SMALL : MOE_DECODE_OK;
 }
 
-GroupedArgs kernel_args(const moe_grouped_args& a, int rows) {
+GroupedArgs kernel_args(const moe_grouped_args& a) {
   GroupedArgs g{};
   g.x = static_cast<const uint8_t*>(a.x);
   g.xs = a.x_scale;
@@ -137,7 +138,7 @@ GroupedArgs kernel_args(const moe_grouped_args& a, int rows) {
   g.N = a.N;
   g.K = a.K;
   g.limit = a.limit;
-  g.splits = a.workspace ? grouped_splits(a.R, a.E, a.N, a.K, rows) : 1;
+  g.splits = a.workspace ? grouped_splits(a.R, a.E, a.N, a.K) : 1;
   g.partial = static_cast<float*>(a.workspace);
   return g;
 }
@@ -148,11 +149,11 @@ GroupedArgs kernel_args(const moe_grouped_args& a, int rows) {
 extern "C" {
 
 size_t moe_grouped_gemm_workspace(int32_t R, int32_t E, int32_t N, int32_t K) {
-  return moe::workspace(R, E, N, K, moe::kProductRows);
+  return moe::workspace(R, E, N, K);
 }
 
 size_t moe_grouped_swiglu_workspace(int32_t R, int32_t E, int32_t N, int32_t K) {
-  return moe::workspace(R, E, N, K, moe::kSwigluRows);
+  return moe::workspace(R, E, N, K);
 }
 
 int moe_grouped_gemm(const moe_grouped_args* args, void* stream) {
@@ -160,9 +161,10 @@ int moe_grouped_gemm(const moe_grouped_args* args, void* stream) {
   if (const int rc = check(args)) return rc;
   if (args->R == 0) return MOE_DECODE_OK;
   if (const int rc = check_workspace(*args, moe_grouped_gemm_workspace(args->R, args->E, args->N, args->K))) return rc;
-  const GroupedArgs a = kernel_args(*args, kProductRows);
+  const GroupedArgs a = kernel_args(*args);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  launch_grouped_product(args->quant == MOE_QUANT_MXFP8, a, s);
+  const auto launch = args->sums == MOE_SUMS_FP8 ? launch_grouped_product_fp8 : launch_grouped_product;
+  launch(args->quant == MOE_QUANT_MXFP8, a, s);
   if (a.splits > 1) launch_join(join_product_kernel, a, a.N, s);
   return hipGetLastError() == hipSuccess ? MOE_DECODE_OK : MOE_DECODE_ERR_HIP;
 }
@@ -170,12 +172,12 @@ int moe_grouped_gemm(const moe_grouped_args* args, void* stream) {
 int moe_grouped_swiglu(const moe_grouped_args* args, void* stream) {
   using namespace moe;
   if (const int rc = check(args)) return rc;
-  if (args->N % 256) return MOE_DECODE_ERR_UNSUPPORTED;
+  if (args->N % 256 || args->sums != MOE_SUMS_FP32) return MOE_DECODE_ERR_UNSUPPORTED;
   if (!(args->limit > 0.f)) return MOE_DECODE_ERR_INVALID_ARG;
   if (args->R == 0) return MOE_DECODE_OK;
   if (!args->out_scale || misaligned(args->out_scale, 4)) return MOE_DECODE_ERR_INVALID_ARG;
   if (const int rc = check_workspace(*args, moe_grouped_swiglu_workspace(args->R, args->E, args->N, args->K))) return rc;
-  const GroupedArgs a = kernel_args(*args, kSwigluRows);
+  const GroupedArgs a = kernel_args(*args);
   hipStream_t s = static_cast<hipStream_t>(stream);
   launch_grouped_swiglu(args->quant == MOE_QUANT_MXFP8, a, s);
   if (a.splits > 1) launch_join(join_swiglu_kernel, a, a.N / 2, s);

@@ -1,19 +1,7 @@
 // moe_grouped_swiglu: up to 128 rows of an expert by 128 hidden columns (256
-// weight rows, up and gate) per workgroup.
-//
-// Every 128-wide K block of the tile's activations and weights is copied into
-// LDS (up to 48 KB, three blocks at a time), read from there by eight waves, 64
-// rows by 32 up and 32 gate columns each, widened to BF16 (exact) and multiplied
-// by the 32x32x16 instruction; the block's FP32 sums are multiplied by its
-// scales when they are added. BF16 and not the FP8 instruction, because the
-// hidden's codes and scales are decided from these sums: the FP8 instruction
-// adds eight products at a time cut off 14 bits below the largest (measured;
-// 2^-16 of a result on average), which moves an FP32 scale by 1e-5, ten times
-// what FP32 sums do. F16 is as exact (both keep 23 bits below the largest), but
-// a hundredth slower (4.61 and 4.56 ms for 65,536 rows over 256 experts, K =
-// 7168, I = 2048) and too narrow for MXFP8 scales that lie 2^15 and more apart.
-// The two halves of the waves share the tile's 32-row groups evenly, a SIMD has
-// one wave of each, and row tiles of an expert are alike in size.
+// weight rows, up and gate) per workgroup, by grouped_tile.h's tile: the hidden's
+// codes and scales are decided from its sums, and sums of the FP8 instruction
+// would move an FP32 scale by 1e-5, ten times what FP32 sums do.
 //
 // Bounds, measured on MI355X. Few rows: the weights' bytes (4 tokens x 8 of 256
 // experts, K = 7168, I = 2048: 134 us, 6.7 TB/s). Many: the matrix
@@ -26,273 +14,15 @@
 // at 12, so there is one size.
 #include <hip/hip_runtime.h>
 
-#include <type_traits>
-
-#include "grouped_device.h"
+#include "grouped_tile.h"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kGroup = 32;  // rows of a matrix instruction
-constexpr int kRows = kSwigluRows;
-constexpr int kStages = 3;  // K blocks in LDS: one read, the others on their way
-
-// A K block in LDS, for waves of up to kFirst 32-row groups.
-template <int kFirst>
-struct Stage {
-  uint8_t x[2 * kFirst * kGroup * 128];
-  uint8_t w[256 * 128];
-  uint32_t xs[2 * kFirst * kGroup];  // FP32 scales, or four E8M0 bytes
-};
-struct Shared {
-  alignas(16) uint8_t st[kStages * sizeof(Stage<2>)];
-  float amax[4][kRows];
-};
-
-typedef float float16_t __attribute__((ext_vector_type(16)));
-
-// Sixteen codes of a row in BF16, two instructions' worth.
-struct Wide16 {
-  bf16x8_t v[2];
-};
-__device__ __forceinline__ Wide16 widen16(const u32x4_t& q, float scale) {
-  return Wide16{{widen8_scaled(q[0], q[1], scale), widen8_scaled(q[2], q[3], scale)}};
-}
-
-// kJ: the 32-row groups of this wave; kFirst: those of the first four waves.
-template <bool kMx, bool kWhole, int kFirst, int kJ>
-__device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Shared& sm) {
-  constexpr int kHalf = kFirst * kGroup;  // LDS rows of a half of the waves
-  const Stage<kFirst>* const stage = reinterpret_cast<const Stage<kFirst>*>(sm.st);
-  constexpr int kN = kJ ? kJ : 1;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int r32 = lane & 31, h = lane >> 5;
-  const int wn = wave & 3, wm = wave >> 2;
-  const int I = a.N / 2, tile_col = kWhole ? at.col : at.col / a.splits;
-  const KPart part = k_part<kWhole>(a, at);
-  const int KB = part.blocks;
-
-  // What this wave copies of a block: 32 LDS rows of the weights, 8 kFirst
-  // of the activations and 64 scales (the same ones by several waves, so that
-  // every wave has as many copies on its way). LDS row L keeps 16-byte chunk c of its
-  // row at place c ^ (L / 2 % 8), so that the 16 rows of a read phase differ in
-  // bank. A wave's results of an instruction are weight rows 8 a + 4 h + b (a,
-  // b = 0..3) of its 32: these are columns 16 h + 4 a + b, so that a lane's 16
-  // are neighbours.
-  constexpr int kXCopies = kFirst, kCopies = 4 + kXCopies + 1;
-  const int lr = lane >> 3;
-  const auto x_of = [&](int L) {  // activation row of LDS row L
-    return (size_t)max(x_row(a, min(at.row + L, at.end - 1)), 0);
-  };
-  const uint8_t* xp[kXCopies];
-#pragma unroll
-  for (int i = 0; i < kXCopies; ++i) {
-    const int L = (wave * kXCopies + i) * 8 + lr;
-    xp[i] = a.x + x_of(L) * a.K + (size_t)part.first * 128 + ((lane & 7) ^ ((L >> 1) & 7)) * 16;
-  }
-  // up rows for even waves, the same columns' gate rows for odd ones; its
-  // eight LDS rows i begin 4 i columns further, at the other half's chunks
-  // where i is odd
-  const uint8_t* wp = a.w + ((size_t)at.e * a.N + tile_col * 128 + (wave >> 1) * 32 + (wave & 1) * I) * a.K + (size_t)part.first * 128;
-  const uint32_t wrow = (uint32_t)((lr >> 2) * 16 + (lr & 3)) * (uint32_t)a.K, chunk = ((lane & 7) ^ (lr >> 1)) * 16;
-  const uint32_t woff[2] = {wrow + chunk, wrow + (chunk ^ 64)};
-  const int sl = wave % kFirst * 64;  // its first scale
-  const uint8_t* sp = static_cast<const uint8_t*>(a.xs) + (x_of(sl + lane) * (a.K / 128) + part.first) * 4;
-  const uint32_t lds = lds_offset(sm.st);
-  const auto issue = [&](int st, int b) {
-    const int kb = part.at<kWhole>(b);
-    const uint32_t to = lds + st * (uint32_t)sizeof(Stage<kFirst>);
-    const size_t k0 = (size_t)kb * 128;
-    const auto weights = [&](auto once) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        copy16_to_lds<decltype(once)::value>(wp + k0 + (size_t)(4 * i) * a.K, woff[i & 1],
-                                             to + (uint32_t)offsetof(Stage<kFirst>, w) + (wave * 32 + i * 8) * 128);
-    };
-    if (at.only)
-      weights(std::true_type{});
-    else
-      weights(std::false_type{});
-#pragma unroll
-    for (int i = 0; i < kXCopies; ++i) copy16_to_lds(xp[i] + k0, to + (wave * kXCopies + i) * 1024);
-    copy4_to_lds(sp + (size_t)kb * 4, to + (uint32_t)offsetof(Stage<kFirst>, xs) + sl * 4);
-  };
-
-  const uniform_floats su = as_uniform(a.ws) + ((size_t)at.e * (a.N / 128) + tile_col) * (a.K / 128) + part.first;
-  const uniform_floats sg = su + (size_t)(I / 128) * (a.K / 128);
-
-  // Sixteen bytes of every row (chunk h + 2 c of the lane's row) at a time,
-  // widened while the matrix instructions of the chunk before run. Of a
-  // wave's two products [t], 0 is up and 1 gate.
-  const float16_t zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  int off[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) off[c] = r32 * 128 + (((h + 2 * c) ^ (r32 >> 1)) & 7) * 16;
-  Wide16 w[2][2], x[2][kN];  // [chunk parity]
-  float rel[kN][4], xs[kN];
-  float16_t acc[kN][2], p[kN][2];
-#pragma unroll
-  for (int j = 0; j < kJ; ++j) acc[j][0] = acc[j][1] = zero;
-  const auto scales = [&](int st) {
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-      const uint32_t sx = stage[st].xs[wm * kHalf + j * 32 + r32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) rel[j][c] = 1.f;
-      xs[j] = kMx ? mx_scales(sx, rel[j]) : __uint_as_float(sx);
-    }
-  };
-  const auto load = [&](int st, int c) {
-    if (!kJ) return;
-    const uint8_t *wb = stage[st].w + wn * 64 * 128, *xb = stage[st].x + wm * kHalf * 128;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) w[c & 1][t] = widen16(*reinterpret_cast<const u32x4_t*>(wb + t * 4096 + off[c]), 1.f);
-#pragma unroll
-    for (int j = 0; j < kJ; ++j)
-      x[c & 1][j] = widen16(*reinterpret_cast<const u32x4_t*>(xb + j * 4096 + off[c]), rel[j][c]);
-  };
-  const auto multiply = [&](int c) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < kJ; ++j)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          p[j][t] =
-              __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[c & 1][t].v[i], x[c & 1][j].v[i], c || i ? p[j][t] : zero, 0, 0, 0);
-  };
-  // Block b's copies have ended, in every wave, and every wave has read all
-  // of the block before. The copies of kStages - 2 blocks behind may be on
-  // their way.
-  const auto ready = [&](int b) {
-    if (b + kStages - 2 < KB)
-      copies_left<(kStages - 2) * kCopies>(&sm);
-    else
-      copies_left<0>(&sm);
-    workgroup_barrier();
-  };
-
-#pragma unroll
-  for (int b = 0; b < kStages - 1; ++b)
-    if (b < KB) issue(b, b);
-  ready(0);
-  if (kStages - 1 < KB) issue(kStages - 1, kStages - 1);
-  scales(0);
-  load(0, 0);
-  int st = 0;
-  for (int b = 0; b < KB; ++b) {
-    const float s0 = su[part.at<kWhole>(b)], s1 = sg[part.at<kWhole>(b)];
-    load(st, 1);
-    multiply(0);
-    load(st, 2);
-    multiply(1);
-    load(st, 3);
-    multiply(2);
-    float sc[kN][2];
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-      sc[j][0] = xs[j] * s0;
-      sc[j][1] = xs[j] * s1;
-    }
-    if (b + 1 < KB) {
-      ready(b + 1);
-      if (b + kStages < KB) issue(st, b + kStages);
-      st = st == kStages - 1 ? 0 : st + 1;
-      scales(st);
-      load(st, 0);
-    }
-    multiply(3);
-#pragma unroll
-    for (int j = 0; j < kJ; ++j)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[j][t][i] = fmaf(p[j][t][i], sc[j][t], acc[j][t][i]);
-  }
-
-  if (!kWhole && a.splits > 1) {
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-      const int i = at.row + (wm * kFirst + j) * kGroup + r32;
-      if (i < at.end) {
-        float* o = a.partial + ((size_t)part.split * a.R + i) * a.N + tile_col * 128 + wn * 32 + h * 16;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<float4_t*>(o + t * I + 4 * q) =
-                float4_t{acc[j][t][4 * q], acc[j][t][4 * q + 1], acc[j][t][4 * q + 2], acc[j][t][4 * q + 3]};
-      }
-    }
-    return;
-  }
-
-  // SwiGLU: a lane's 16 hidden values of a row, the row's maximum over the 128
-  // columns (the row's other lane, then the four waves), the codes
-#pragma unroll
-  for (int j = 0; j < kJ; ++j) {
-    float amax = kAmaxFloor;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float v = swiglu(acc[j][0][i], acc[j][1][i], a.limit);
-      acc[j][0][i] = v;
-      amax = fmaxf(amax, fabsf(v));
-    }
-    amax = fmaxf(amax, __shfl_xor(amax, 32, kWave));
-    if (h == 0) sm.amax[wn][wm * kHalf + j * 32 + r32] = amax;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kJ; ++j) {
-    const int i = at.row + (wm * kFirst + j) * kGroup + r32;
-    if (i < at.end) {
-      float amax = kAmaxFloor;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) amax = fmaxf(amax, sm.amax[q][wm * kHalf + j * 32 + r32]);
-      const bool none = x_row(a, i) < 0;
-      if (none) amax = kAmaxFloor;
-      const float scale = amax / kFp8Max, inv = 1.0f / scale;
-      u32x4_t codes;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        codes[q] = none ? 0u
-                        : e4m3x4_encode_nan(acc[j][0][4 * q] * inv, acc[j][0][4 * q + 1] * inv, acc[j][0][4 * q + 2] * inv,
-                                            acc[j][0][4 * q + 3] * inv);
-      *reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(a.out) + (size_t)i * I + tile_col * 128 + wn * 32 + h * 16) = codes;
-      if (wn == 0 && h == 0) a.outs[(size_t)i * (I / 128) + tile_col] = scale;
-    }
-  }
-}
-
-template <bool kMx, bool kWhole>
-__device__ __forceinline__ void any_tile(const GroupedArgs& a, const TileAt& at, Shared& sm) {
-  // the first half of the waves takes half of the 32-row groups, rounded up,
-  // the other the rest; all branches meet the same barriers
-  const int groups = (at.end - at.row + kGroup - 1) / kGroup, first = (groups + 1) / 2;
-  const bool half = threadIdx.x < kThreads / 2;
-  if (first == 2) {
-    if (half || groups == 4)
-      tile<kMx, kWhole, 2, 2>(a, at, sm);
-    else
-      tile<kMx, kWhole, 2, 1>(a, at, sm);
-  } else if (half || groups == 2) {
-    tile<kMx, kWhole, 1, 1>(a, at, sm);
-  } else {
-    tile<kMx, kWhole, 1, 0>(a, at, sm);
-  }
-}
-
 template <bool kMx>
 __global__ __launch_bounds__(kThreads, 2) void grouped_swiglu_kernel(GroupedArgs a) {
   __shared__ Shared sm;
-  const TileAt at = find_tile<kRows, kGroup, kThreads>(a, blockIdx.x);
-  if (at.e < 0) return;
-  if (whole_k(a, at))
-    any_tile<kMx, true>(a, at, sm);
-  else
-    any_tile<kMx, false>(a, at, sm);
+  grouped_tile<true, kMx>(a, sm);
 }
 
 }  // namespace

@@ -156,10 +156,14 @@ size_t moe_route_rows_workspace(int32_t T, int32_t local_experts);
  *            no access out of bounds
  *   w        [E, N, K] e4m3, w_scale [E, N/128, K/128] FP32
  *   R        rows of the output
- * moe_grouped_gemm: out [R, N] BF16 = g, rounded once. The FP8 matrix
- *   instruction it uses adds the products of eight neighbouring columns cut off
- *   14 bits below the power of two of the largest, and these sums in FP32: off
- *   by some 2^-16 of a row's typical value before the rounding to BF16 (2^-9).
+ * moe_grouped_gemm: out [R, N] BF16 = g, rounded once. With sums =
+ *   MOE_SUMS_FP8 by the FP8 matrix instruction, faster where rows are many: it
+ *   adds the products of eight neighbouring columns cut off 14 bits below the
+ *   power of two of the largest, and these sums in FP32: off by some 2^-16 of a
+ *   row's typical value before the rounding to BF16 (2^-9), but by up to 2^-11 of
+ *   a group's largest product, which is all of the result where the large ones
+ *   cancel; and E8M0 scales may take a block's sum past FP32 before w_scale
+ *   brings it back.
  * moe_grouped_swiglu: w = W13, N = 2I rows (0..I-1 up, I..2I-1 gate):
  *   up = clamp(g[n], +-limit), gate = min(g[I + n], limit),
  *   act = gate / (1 + exp(-gate)) * up,
@@ -183,6 +187,8 @@ size_t moe_route_rows_workspace(int32_t T, int32_t local_experts);
  * (floor(R/128) + E rows of ceil(N/256) tiles). FP8 and output arrays 16-byte aligned, E8M0
  * bytes 4-byte aligned, the others to their element. R = 0 is a valid empty
  * call. */
+#define MOE_SUMS_FP32 0
+#define MOE_SUMS_FP8 1
 typedef struct moe_grouped_args {
   int32_t R, X, E, N, K;
   int32_t quant;     /* of x: MOE_QUANT_FP8, MOE_QUANT_FP8_P2 or MOE_QUANT_MXFP8 */
@@ -197,6 +203,7 @@ typedef struct moe_grouped_args {
   float* out_scale;  /* moe_grouped_swiglu */
   void* workspace;
   size_t workspace_bytes;
+  int32_t sums;      /* moe_grouped_gemm: MOE_SUMS_*; else MOE_SUMS_FP32 */
 } moe_grouped_args;
 int moe_grouped_gemm(const moe_grouped_args* a, void* stream);
 int moe_grouped_swiglu(const moe_grouped_args* a, void* stream);

@@ -490,3 +490,85 @@ def test_weights_past_32_bits():
     g, bound = exact(big, 7 * 2.0**-14)
     bf16 = lambda v: v.float().to(torch.bfloat16).double()  # noqa: E731
     assert ((y.double() >= bf16(g - bound)) & (y.double() <= bf16(g + bound))).all()
+
+
+def bf16(v):
+    return v.float().to(torch.bfloat16).double()
+
+
+def check_gemm_sums(d):
+    """As check_gemm, within the bound of FP32 sums, and closer still on
+    average. The instructions leave a block's sum of 128 off by less than 2^-26
+    of its typical size (measured over random codes), and each of the K/128
+    additions rounds by half a unit at most, at random: sqrt(K/128) * 2^-24,
+    at most 2^-21 of a row's root mean square here. A value that is off by e
+    before its rounding lands on the neighbour, a step away, once in step / 2e
+    times, so the mean square of the rows' distance from the exact ones,
+    rounded, is at most 2 e step; a step is at most 2^-7 of the value:
+    sqrt(2 * 2^-21 * 2^-7) < 2^-13 of the root mean square. The sums of the FP8
+    instruction (2^-16) are twice as far off."""
+    y = call_gemm(d)
+    g, bound = exact(d)
+    got = y[: g.shape[0]].double()
+    bad = (got < bf16(g - bound)) | (got > bf16(g + bound))
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} values outside, first at {torch.nonzero(bad)[0].tolist()}"
+    off = (got - bf16(g)).square().mean().sqrt() / g.square().mean().sqrt()
+    assert off <= 2.0**-13, f"off by {off:.3g} of the root mean square"
+    return y
+
+
+# few rows, all tiles' heights, K split and K turned
+@pytest.mark.parametrize("quant", ["fp8", "mxfp8"])
+@pytest.mark.parametrize("counts,N,K", [([70], 1408, 640), (RAGGED, 640, 1408), (BIG, 384, 1024), ([150, 0, 300], 256, 7168),
+                                        ([(7 * e) % 23 for e in range(38)] + [140, 300], 1024, 4096)],
+                         ids=["one", "ragged", "big", "split", "turned"])
+def test_gemm_sums_in_fp32(counts, N, K, quant):
+    check_gemm_sums(make(counts, N, K, 41, quant, gather=True))
+
+
+@pytest.mark.parametrize("quant", ["fp8", "mxfp8"])
+@pytest.mark.parametrize("counts,N,K", [([3], 128, 128), (BIG, 384, 512), ([5, 0, 140], 256, 2048)], ids=["one", "big", "split"])
+def test_large_products_that_cancel(counts, N, K, quant):
+    """Two products of 448 * 448 of opposite signs in each group of eight
+    columns, the others multiples of 2^-4 up to 7: all sums are multiples of
+    2^-4 below 2^19 and so exact in FP32, and the small products are the
+    result, so the output has to be its BF16 rounding."""
+    d = make(counts, N, K, 42, quant)
+    gen = torch.Generator(device=DEV).manual_seed(43)
+    small = lambda shape: (torch.randint(-7, 8, shape, generator=gen, device=DEV) * 0.25)  # noqa: E731
+    x, w = small(d["x"].shape), small(d["w"].shape)
+    x[:, 0::8], x[:, 5::8] = 448.0, 448.0
+    w[..., 0::8], w[..., 5::8] = 448.0, -448.0
+    d["x"], d["w"] = x.to(F8), w.to(F8)
+    d["w_scale"].fill_(1.0)
+    if quant == "fp8":
+        d["x_scale"].fill_(1.0)
+    else:
+        d["x_scale"].fill_(127)
+    g, _ = exact(d)
+    assert g.abs().max() < 2.0**12
+    assert torch.equal(call_gemm(d)[: g.shape[0]], g.float().to(torch.bfloat16))
+
+
+def fp8_sums(d):
+    return grouped_gemm(d["x"], d["x_scale"], d["w"], d["w_scale"], d["offsets"], rows=d["rows"], sums="fp8")
+
+
+# on the FP8 instruction, within its bound: every tile's height, K split, turned and neither
+@pytest.mark.parametrize("quant", ["fp8", "mxfp8"])
+@pytest.mark.parametrize("counts,N,K", [([1], 128, 128), (RAGGED, 384, 640), (BIG, 384, 640), ([40, 100, 170, 230], 256, 1024),
+                                        ([2, 0, 150, 300], 256, 128 * 37), ([(7 * e) % 23 for e in range(38)] + [140, 300], 1024, 4096)],
+                         ids=["one", "ragged", "big", "heights", "split", "turned"])
+def test_gemm_sums_of_the_fp8_instruction(counts, N, K, quant):
+    d = make(counts, N, K, 44, quant, gather=True)
+    d["rows"][0] = -1
+    y = fp8_sums(d)
+    g, bound = exact(d, 7 * 2.0**-14)
+    n = g.shape[0]
+    got = y[:n].double()
+    assert ((got >= bf16(g - bound)) & (got <= bf16(g + bound))).all()
+    assert not y[0].any() and torch.equal(fp8_sums(d)[:n], y[:n])
+    d["x"].view(torch.uint8)[int(d["rows"][n - 1]), 77] = 0x7F
+    nan = (d["rows"][:n] == d["rows"][n - 1]) & (d["rows"][:n] >= 0)
+    z = fp8_sums(d)[:n]
+    assert torch.isnan(z[nan]).all() and torch.equal(z[~nan], y[:n][~nan])

@@ -131,6 +131,16 @@ def test_grouped_own_errors(L):
     assert L.moe_grouped_swiglu(fill(_rows.GroupedArgs, GROUPED, dict(out_scale=None)), None) == INVALID
 
 
+def test_grouped_sums(L):
+    # the kind of sums is the plain product's own choice
+    for sums in (-1, 2):
+        assert L.moe_grouped_gemm(fill(_rows.GroupedArgs, GROUPED, dict(sums=sums)), None) == UNSUPPORTED
+    for sums in (-1, 1, 2):
+        assert L.moe_grouped_swiglu(fill(_rows.GroupedArgs, GROUPED, dict(sums=sums)), None) == UNSUPPORTED
+    with pytest.raises(ValueError, match="sums"):
+        pkg.grouped_gemm(*grouped_args(), sums="bf16")
+
+
 def test_grouped_workspace(L):
     """Something where K can be split over workgroups, nothing where the tiles
     fill the GPU or K is short; too little of it and a misaligned one are
