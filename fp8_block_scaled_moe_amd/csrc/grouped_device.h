@@ -231,15 +231,38 @@ __device__ __forceinline__ bf16x8_t widen8_scaled(uint32_t w0, uint32_t w1, floa
   return bf16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-// MXFP8 scales from a row's four E8M0 bytes of a block (32 positions each): the
-// largest as the block's own scale, the four relative to it, so that no
-// product is larger than FP32's range allows while its result is not.
-__device__ __forceinline__ float mx_scales(uint32_t bytes, float (&rel)[4]) {
-  const auto byte = [&](int b) { return (int)((bytes >> (8 * b)) & 0xFFu); };
-  const int top = max(max(byte(0), byte(1)), max(byte(2), byte(3)));
+// 2^(byte - 127) of E8M0 byte c of a row's four of a block (32 positions each).
+__device__ __forceinline__ int e8m0_byte(uint32_t bytes, int c) { return (int)((bytes >> (8 * c)) & 0xFFu); }
+__device__ __forceinline__ float e8m0_value(int byte) { return __uint_as_float(byte ? (uint32_t)byte << 23 : 0x400000u); }
+
+// MXFP8 scales of a row's block: the largest as the block's own scale, the four
+// relative to it, so that no product is larger than FP32's range allows while
+// its result is not. A product of two codes is a multiple of 2^-18, so down to a
+// relative scale of 2^-96 every operand is a normal BF16 value and no bit of a
+// product falls out of FP32; and a scale of 2^63 times w_scale is finite up to
+// 2^64. Beyond either (`far`), each 32 positions are to be summed and scaled by
+// themselves (scale_apart); the relative scales and the block's own are 1 and 0 then.
+constexpr int kMxApart = 96, kMxTop = 127 + 63;
+__device__ __forceinline__ float mx_scales(uint32_t bytes, float (&rel)[4], bool& far) {
+  int top = 0, bottom = 255;
 #pragma unroll
-  for (int b = 0; b < 4; ++b) rel[b] = __uint_as_float((uint32_t)max(127 + byte(b) - top, 1) << 23);
-  return __uint_as_float(top ? (uint32_t)top << 23 : 0x400000u);
+  for (int c = 0; c < 4; ++c) {
+    top = max(top, e8m0_byte(bytes, c));
+    bottom = min(bottom, e8m0_byte(bytes, c));
+  }
+  far = top - bottom > kMxApart || top > kMxTop;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) rel[c] = far ? 1.f : __uint_as_float((uint32_t)(127 + e8m0_byte(bytes, c) - top) << 23);
+  return far ? 0.f : e8m0_value(top);
+}
+
+// s * 2^(byte - 127) in two factors, the second 2^up with up >= 0, so that the
+// first is finite and a sum scaled by both is what it would be without FP32's
+// limits.
+__device__ __forceinline__ float scale_apart(float s, int byte, int& up) {
+  const int e = (int)((__float_as_uint(s) >> 23) & 0xFFu) - 127;
+  up = max(byte - 127 + e - 126, 0);
+  return ldexpf(s, byte - 127 - up);
 }
 
 // gate / (1 + exp(-gate)) * up with both clamped. A clamped NaN stays one.

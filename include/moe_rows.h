@@ -147,7 +147,8 @@ size_t moe_route_rows_workspace(int32_t T, int32_t local_experts);
  * with FP32 sums.
  *   x        [X, K] e4m3 with x_scale [X, K/128] FP32 (MOE_QUANT_FP8 or
  *            MOE_QUANT_FP8_P2) or [X, K/32] E8M0 bytes (MOE_QUANT_MXFP8);
- *            no E8M0 byte 255
+ *            no E8M0 byte 255. Scales whose product with w_scale is finite
+ *            (MXFP8: any, with w_scale below 2^64)
  *   rows     [R] int32 or NULL (then X >= R); an index outside [0, X) gives
  *            a row of zeros
  *   offsets  [E + 1] int32, ascending from 0 to at most R; rows from

@@ -572,3 +572,58 @@ def test_gemm_sums_of_the_fp8_instruction(counts, N, K, quant):
     nan = (d["rows"][:n] == d["rows"][n - 1]) & (d["rows"][:n] >= 0)
     z = fp8_sums(d)[:n]
     assert torch.isnan(z[nan]).all() and torch.equal(z[~nan], y[:n][~nan])
+
+
+def far_apart(counts, N, K, seed, apart, zeros, every=1):
+    """A block's second 32 positions with a scale 2^apart above the others',
+    whose codes (`zeros` "x") or whose weights ("w") are zero, in every
+    `every`-th row (the others have scales alike), and weight scales that make the
+    results of the order of one."""
+    d = make(counts, N, K, seed, "mxfp8")
+    gen = torch.Generator(device=DEV).manual_seed(seed + 1)
+    low = min(100, 254 - apart)
+    s = torch.randint(max(low - 4, 0), low + 1, d["x_scale"].shape, generator=gen, device=DEV)
+    s[::every, 1::4] = low + apart
+    d["x_scale"] = s.to(torch.uint8)
+    d["w_scale"] *= 2.0 ** (127 - low) / 100.0
+    at = (torch.arange(K, device=DEV) // 32) % 4 == 1
+    if zeros == "x":
+        d["x"].view(torch.uint8)[::every, at] = 0
+    else:
+        d["w"].view(torch.uint8)[..., at] = 0
+    return d
+
+
+@pytest.mark.parametrize("zeros", ["x", "w"])
+@pytest.mark.parametrize("apart", [64, 96, 97, 112, 120, 126, 127, 160, 254])
+@pytest.mark.parametrize("counts,N,K", [([3, 40], 256, 512), ([150, 20, 300], 256, 256), ([2, 33], 256, 2048 + 128)],
+                         ids=["few", "many", "split"])
+def test_e8m0_scales_any_distance_apart(counts, N, K, apart, zeros):
+    d = far_apart(counts, N, K, 45, apart, zeros)
+    assert not torch.isnan(check_gemm(d, 2.0**-126)[: sum(counts)]).any()
+    check_swiglu(d)
+
+
+@pytest.mark.parametrize("counts", [[3, 40], [150, 20, 300]], ids=["few", "many"])
+def test_rows_with_scales_far_apart_beside_others(counts):
+    """Every third row only: each is right, and the others have the bits that
+    they have among their like."""
+    d = far_apart(counts, 512, 384, 47, 140, "x", every=3)
+    y, (h, s) = check_gemm(d, 2.0**-126), check_swiglu(d)
+    d["x_scale"][::3, 1::4] = d["x_scale"][::3, 0::4]  # nothing far apart any more
+    y2, (h2, s2) = check_gemm(d), check_swiglu(d)
+    n = sum(counts)
+    keep = torch.arange(n, device=DEV) % 3 != 0
+    assert torch.equal(y[:n][keep], y2[:n][keep])
+    assert torch.equal(h[:n][keep], h2[:n][keep]) and torch.equal(s[:n][keep], s2[:n][keep])
+
+
+@pytest.mark.parametrize("counts", [[3, 40], [150, 20, 300]], ids=["few", "many"])
+def test_e8m0_bytes_from_0_to_230(counts):
+    """Bytes all over the range, 0 among them: the largest of a row decide."""
+    d = make(counts, 256, 512, 48, "mxfp8")
+    gen = torch.Generator(device=DEV).manual_seed(49)
+    d["x_scale"] = torch.randint(0, 231, d["x_scale"].shape, generator=gen, device=DEV).to(torch.uint8)
+    d["w_scale"] *= 2.0**-110
+    check_gemm(d, 2.0**-126)
+    check_swiglu(d)
