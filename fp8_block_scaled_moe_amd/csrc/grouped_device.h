@@ -265,11 +265,17 @@ __device__ __forceinline__ float scale_apart(float s, int byte, int& up) {
   return ldexpf(s, byte - 127 - up);
 }
 
-// gate / (1 + exp(-gate)) * up with both clamped. A clamped NaN stays one.
+// gate / (1 + exp(-gate)) * up with both clamped. A clamped NaN stays one. The
+// exponential by the hardware's exp2 of gate log2 e, whose rounding (and that of
+// log2 e) is made up for to first order, so that its error does not grow with
+// |gate|; below -87 a gate counts as -87, whose SiLU is 2^-119.
 __device__ __forceinline__ float swiglu(float up, float gate, float limit) {
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
   up = up != up ? up : __builtin_amdgcn_fmed3f(up, -limit, limit);
-  gate = gate > limit ? limit : gate;
-  const float e = __builtin_amdgcn_exp2f(gate * -1.44269504088896341f);
+  gate = gate != gate ? gate : __builtin_amdgcn_fmed3f(gate, -87.f, limit);
+  const float t = gate * -kLog2e, rest = fmaf(gate, -kLog2eRest, fmaf(gate, -kLog2e, -t));
+  float e = __builtin_amdgcn_exp2f(t);
+  e = fmaf(e, rest * kLn2, e);
   return gate * __builtin_amdgcn_rcpf(1.f + e) * up;
 }
 

@@ -627,3 +627,29 @@ def test_e8m0_bytes_from_0_to_230(counts):
     d["w_scale"] *= 2.0**-110
     check_gemm(d, 2.0**-126)
     check_swiglu(d)
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_swiglu_exponential(split):
+    """One hidden value a row, gate -+x and up x / 4 for a scale x of the row,
+    so that the hidden's scale tells it: gates from -20 to 7, none less exact
+    than others. The exponential is within a unit of 2^-23 and a half, 1 + e, the
+    two products and the division by 448 round by a half each and the reciprocal is
+    within a unit: 4.5 units, 5 with their products."""
+    K = 2048 if split else 128
+    R = 4000 if not split else 200
+    gen = torch.Generator(device=DEV).manual_seed(50)
+    xs = torch.rand(R, generator=gen, device=DEV) * 20.0 + 0.01
+    one = torch.tensor(1.0, device=DEV).to(F8)
+    x, w = torch.zeros(R, K, device=DEV).to(F8), torch.zeros(2, 256, K, device=DEV).to(F8)
+    x[:, 5] = one
+    w[:, 7, 5] = (one.float() / 4).to(F8)            # up
+    w[0, 128 + 7, 5], w[1, 128 + 7, 5] = one, (-one.float()).to(F8)  # gate
+    scale = torch.ones(R, K // 128, device=DEV)
+    scale[:, 0] = xs
+    offsets = torch.tensor([0, R // 2, R], dtype=torch.int32, device=DEV)
+    _, s = grouped_swiglu(x, scale, w, torch.ones(2, 2, K // 128, device=DEV), offsets, limit=7.0)
+    g = torch.where(torch.arange(R, device=DEV) < R // 2, xs, -xs).double().clamp_max(7.0)
+    act = (g * torch.sigmoid(g) * (xs.double() / 4)).abs()
+    assert act.min() > 1e-9
+    assert ((s[:, 0].double() * 448.0 - act).abs() <= act * 5 * 2.0**-23).all()
