@@ -5,7 +5,10 @@ Argument checks and marshalling only. Every call allocates its outputs (and
 all but the norm a workspace where one is needed) from torch's caching
 allocator and launches on the current stream of the tensors' device, or on
 `stream` when one is given; it never synchronises, so it can be captured into
-a graph.
+a graph. With `stream`, as under torch.cuda.stream, the outputs are that
+stream's: its work has to be behind what wrote the inputs, and whoever reads the
+outputs on another stream waits for it and records them there. The inputs are
+recorded on it by the call.
 """
 
 from __future__ import annotations
@@ -79,8 +82,10 @@ def _on_gpu(dev: torch.device) -> None:
 
 
 @contextlib.contextmanager
-def _place(dev, stream):
-    """Makes dev, and stream if one is given, current."""
+def _place(dev, stream, inputs):
+    """Makes dev, and stream if one is given, current; `inputs` are recorded on
+    that stream, so that their memory is not handed out anew before it is
+    through with them."""
     with torch.cuda.device(dev):
         if stream is None:
             yield
@@ -91,6 +96,9 @@ def _place(dev, stream):
                 raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
             with torch.cuda.stream(stream):
                 yield
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
 
 
 class _Here:
@@ -106,9 +114,9 @@ class _Here:
 _here = _Here()
 
 
-def _where(dev, stream):
+def _where(dev, stream, *inputs):
     _on_gpu(dev)
-    return _here if stream is None and dev.index == torch.cuda.current_device() else _place(dev, stream)
+    return _here if stream is None and dev.index == torch.cuda.current_device() else _place(dev, stream, inputs)
 
 
 # The current stream's handle without an object around it, where this torch
@@ -178,7 +186,7 @@ def add_rmsnorm_quant(residual: Optional[torch.Tensor], gamma: Optional[torch.Te
         raise ValueError(f"D must be a multiple of {unit} up to {ROWS_MAX_D} and top_k at most 32, got D={D}, k={k}")
     if not (want_residual or want_out or quant is not None):
         raise ValueError("no output is wanted")
-    with _where(dev, stream):
+    with _where(dev, stream, residual, gamma, delta, y, pos, weights):
         if like.shape == (T, D):
             new = lambda dtype: torch.empty_like(like, dtype=dtype)  # noqa: E731
         else:
@@ -215,7 +223,7 @@ def route_rows(logits: torch.Tensor, bias: torch.Tensor, *, top_k: int, routed_s
         raise ValueError(f"1 <= E <= 1024 and 1 <= top_k <= min(E, 32) are needed, got E={E}, top_k={top_k}")
     if not (local_begin >= 0 and El >= 1 and local_begin + El <= E):
         raise ValueError(f"local experts [{local_begin}, {local_begin + El}) must lie in [0, {E})")
-    with _where(dev, stream):
+    with _where(dev, stream, logits, bias):
         ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
         pos, weights = torch.empty_like(ids), torch.empty_like(ids, dtype=torch.float32)
         offsets, rows = ids.new_empty(El + 1), ids.new_empty(T * top_k)
@@ -274,7 +282,7 @@ def grouped_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scal
     if sums not in SUMS:
         raise ValueError(f"sums must be one of {list(SUMS)}, got {sums!r}")
     dev, R, sizes, ptrs = _grouped(x, x_scale, w, w_scale, offsets, rows)
-    with _where(dev, stream):
+    with _where(dev, stream, x, x_scale, w, w_scale, offsets, rows):
         out = torch.empty((R, sizes[3]), dtype=torch.bfloat16, device=dev)
         if R:
             need = lib().moe_grouped_gemm_workspace(R, *sizes[2:5])
@@ -296,7 +304,7 @@ def grouped_swiglu(x: torch.Tensor, x_scale: torch.Tensor, w13: torch.Tensor, w1
     if not limit > 0:
         raise ValueError(f"limit must be positive, got {limit}")
     I = sizes[3] // 2
-    with _where(dev, stream):
+    with _where(dev, stream, x, x_scale, w13, w13_scale, offsets, rows):
         h = torch.empty((R, I), dtype=torch.uint8, device=dev)
         scale = torch.empty((R, I // 128), dtype=torch.float32, device=dev)
         if R:

@@ -234,3 +234,61 @@ def test_padded_batch():
     pad.g1, pad.g2 = blk.g1, blk.g2
     got = [t[:100] for t in pad.run()]
     assert same([t.contiguous() for t in got], want)
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_inputs_let_go_while_another_stream_needs_them(raw):
+    """Inputs that the caller drops right after a call on a stream that has not
+    begun with it keep their memory until that stream is through."""
+    blk = Block(50, 60)
+    inp, sh = blk.inp, SHAPE
+    q, xs = quantise(inp.x)
+    r = route_rows(inp.logits, inp.bias, top_k=sh.top_k, routed_scale=sh.routed_scale)
+    h, hs = grouped_swiglu(q, xs, inp.w13, inp.w13_scale, r.offsets, limit=sh.limit, rows=r.rows)
+    y = grouped_gemm(h, hs, inp.w2, inp.w2_scale, r.offsets)
+    calls = [
+        (add_rmsnorm_quant, (blk.residual, blk.g1), dict(delta=blk.delta)),
+        (add_rmsnorm_quant, (blk.residual, blk.g2), dict(y=y, pos=r.pos, weights=r.weights)),
+        (route_rows, (inp.logits, inp.bias), dict(top_k=sh.top_k, routed_scale=sh.routed_scale)),
+        (grouped_swiglu, (q, xs, inp.w13, inp.w13_scale, r.offsets), dict(limit=sh.limit, rows=r.rows)),
+        (grouped_gemm, (h, hs, inp.w2, inp.w2_scale, r.offsets), {}),
+    ]
+    copy = lambda v: v.clone() if isinstance(v, torch.Tensor) else v  # noqa: E731
+    flat = lambda out: list(out) if isinstance(out, tuple) else [out]  # noqa: E731
+    for call, args, kw in calls:
+        want = bits(flat(call(*args, **kw)))
+        s = torch.cuda.Stream()
+        mine, mkw = [copy(v) for v in args], {n: copy(v) for n, v in kw.items()}
+        like = [v for v in (*mine, *mkw.values()) if isinstance(v, torch.Tensor)]
+        at = {v.data_ptr() for v in like}
+        shapes = [(v.shape, v.dtype) for v in like]
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        got = flat(call(*mine, **mkw, stream=s.cuda_stream if raw else s))
+        del mine, mkw, like
+        new = [torch.empty(n, dtype=d, device=DEV) for n, d in shapes]
+        for t in new:
+            t.view(torch.uint8).fill_(0x11)
+        assert not at & {t.data_ptr() for t in new}
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_graph_captured_with_the_stream_given():
+    """A capture on a stream that the calls are given too."""
+    blk = Block(51, 70)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    blk.run(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = blk.run(s)
+    for seed in range(3):
+        blk.residual.copy_(torch.randn(blk.residual.shape, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = bits(out)
+        assert same(replayed, blk.run())
+        torch.cuda.synchronize()
