@@ -178,10 +178,9 @@ __device__ __forceinline__ int x_row(const GroupedArgs& a, int i) {
 // Copies from memory straight into LDS: lane l's 16 (or 4) bytes go to byte
 // 16 l (4 l) behind `to`, the same for the whole wave. In assembly, since the
 // compiler waits for its own form of them before every later read of LDS,
-// whichever buffer it reads; no register is written but M0, which nothing else
-// uses on this target, and copies_left() waits until at most n of the wave's
-// are on their way (they end in order). A workgroup barrier behind it makes
-// all waves' copies visible.
+// whichever buffer it reads; no register is written but M0, and copies_left()
+// waits until at most n of the wave's are on their way (they end in order). A
+// workgroup barrier behind it makes all waves' copies visible.
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
@@ -191,10 +190,10 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
   return reinterpret_cast<const uint8_t*>(((uint64_t)uniform((uint32_t)(v >> 32)) << 32) | uniform((uint32_t)v));
 }
 __device__ __forceinline__ void copy16_to_lds(const uint8_t* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uniform(to)), "v"(from));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uniform(to)), "v"(from) : "m0");
 }
 __device__ __forceinline__ void copy4_to_lds(const uint8_t* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform(to)), "v"(from));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform(to)), "v"(from) : "m0");
 }
 // The same from a uniform address plus the lane's offset. kOnce: with the
 // non-temporal hint, for data that is read once: weights of an expert's only
@@ -205,10 +204,10 @@ template <bool kOnce>
 __device__ __forceinline__ void copy16_to_lds(const uint8_t* base, uint32_t offset, uint32_t to) {
   if (kOnce)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(uniform(to)), "v"(offset),
-                 "s"(uniform(base)));
+                 "s"(uniform(base)) : "m0");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform(to)), "v"(offset),
-                 "s"(uniform(base)));
+                 "s"(uniform(base)) : "m0");
 }
 // At most kLeft copies are left, and all reads of LDS have returned.
 template <int kLeft>

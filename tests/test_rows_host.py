@@ -308,3 +308,17 @@ def test_grouped_binding_refuses_options():
     args[0], args[1] = args[0][:0], args[1][:0]
     with pytest.raises(ValueError, match="no rows"):
         pkg.grouped_gemm(*args, rows=torch.zeros(2, dtype=torch.int32))
+
+
+def test_assembly_names_the_registers_it_writes():
+    """Every asm statement that writes M0 says so: the compiler uses it too."""
+    import re
+
+    csrc, seen = os.path.join(ROOT, "fp8_block_scaled_moe_amd", "csrc"), 0
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name)) as f:
+            for stmt in re.findall(r"asm volatile\(.*?\);", f.read(), re.S):
+                if "s_mov_b32 m0" in stmt:
+                    seen += 1
+                    assert re.search(r':\s*"m0"', stmt), f"{name}: {stmt}"
+    assert seen
