@@ -201,3 +201,21 @@ def test_same_bits_alone_and_in_a_batch():
     one = {n: (v[40:41] if n in ("residual", "delta", "pos", "weights") else v) for n, v in d.items()}
     for a, b in zip(add_rmsnorm_quant(eps=EPS, **device(one)), whole):
         assert torch.equal(a[0], b[40])
+
+
+# plain rows of more than 512 tokens have narrower workgroups, up to four chunks a lane
+@pytest.mark.parametrize("quant", ["fp8", "fp8_p2", "mxfp8"])
+@pytest.mark.parametrize("D", WIDTHS)
+def test_widths_of_many_tokens(D, quant):
+    check(make(513, D, 0, D + 1), quant)
+
+
+@pytest.mark.parametrize("D,quant", [(8, None), (2056, None), (4104, None), (4096 + 96, "mxfp8"), (8192 + 32, "mxfp8"), (16376, None)])
+def test_narrow_units_of_many_tokens(D, quant):
+    check(make(600, D, 0, D + 2), quant)
+
+
+@pytest.mark.parametrize("D", [2176, 7168])
+@pytest.mark.parametrize("T", [512, 513, 4096])
+def test_tokens_around_the_narrow_workgroups(T, D):
+    check(make(T, D, 0, T + D), "fp8")
