@@ -6,9 +6,12 @@
 // the bound is HBM (8,191 rows of 3584 with an addend, MXFP8: 54 us, 4.9 TB/s;
 // 4,096 rows of 7168 with eight routed rows each: 142 us, 4.8 TB/s; a large copy
 // runs at 4.9). The sum and the sum of squares are taken in FP64 (two
-// more instructions per value, hidden behind memory), which makes the FP32
-// row the correctly rounded sum whatever the order, and the codes and scales
-// the same on every run and for every workgroup size.
+// more instructions per value, hidden behind memory): residual, addend, then the
+// picks in their order, rounded to FP32. That is the correctly rounded sum but
+// next to a rounding border and where terms of 2^29 times the result and more
+// cancel; the same call gives the same bits every time. The sum of squares is
+// joined over a workgroup's lanes, so the last bit of rstd may differ, next to a
+// rounding border, between the workgroup sizes of the launch below.
 #include <hip/hip_runtime.h>
 
 #include "../../include/moe_rows.h"

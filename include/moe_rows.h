@@ -62,10 +62,13 @@ extern "C" {
  * page, epilogue (FP8 per 128), nvfp4-megamoe-kernel README (routing weights
  * applied once, to the unweighted expert rows). For each token t:
  *   h = residual[t] + delta[t] + sum_j weights[t, j] * y[pos[t, j]]
- *       summed in FP64, rounded once to FP32 (so it does not depend on the
- *       order); a position outside [0, R) adds nothing (expert not local);
+ *       summed in FP64 in this order and rounded to FP32: the correctly
+ *       rounded sum but next to a rounding border and where terms of 2^29 times
+ *       the result and more cancel; a position outside [0, R) adds nothing (expert not local);
  *   residual_out[t] = BF16(h);
- *   rstd = FP32(1 / sqrt(sum_i h_i^2 / D + eps)), the statistics in FP64;
+ *   rstd = FP32(1 / sqrt(sum_i h_i^2 / D + eps)), the statistics in FP64
+ *       (T and k choose the order of this sum, which may move rstd's last bit
+ *       next to a rounding border; the same call gives the same bits);
  *   v = (h * rstd) * gamma, two FP32 products (v = h when gamma is NULL);
  *   out[t] = BF16(v); q[t], scale[t] = the 8-bit form of v (not of BF16(v)).
  *   residual     [T, D] BF16, or NULL (0)

@@ -219,3 +219,27 @@ def test_narrow_units_of_many_tokens(D, quant):
 @pytest.mark.parametrize("T", [512, 513, 4096])
 def test_tokens_around_the_narrow_workgroups(T, D):
     check(make(T, D, 0, T + D), "fp8")
+
+
+def test_order_of_a_cancelling_sum():
+    """Terms 2^54 and more above what is left of them: residual, addend, then the
+    picks as they come, each addition rounded to FP64 (the products of a weight and
+    a value are exact there)."""
+    d = make(40, 256, 4, 14, spread=False)
+    rng = np.random.default_rng(15)
+    big = 2.0 ** rng.integers(54, 70, size=(40, 256))
+    y = d["y"].copy()
+    for a, b in ((0, 2), (1, 3), (3, 0)):
+        at = slice(0, 20) if (a, b) == (0, 2) else slice(20, 30) if (a, b) == (1, 3) else slice(30, 40)
+        y[d["pos"][at, a]], y[d["pos"][at, b]] = big[at], -big[at]
+        d["weights"][at, b] = d["weights"][at, a]
+    d["y"] = y
+    h = d["residual"].astype(np.float64) + d["delta"]
+    for j in range(4):
+        h = h + d["weights"][:, j : j + 1].astype(np.float64) * y[d["pos"][:, j]]
+    res, _, _, _ = add_rmsnorm_quant(eps=EPS, quant=None, want_out=False, **device(d))
+    assert np.array_equal(host(res), bf16_round(h.astype(np.float32).astype(np.float64)))
+    back = d["residual"].astype(np.float64) + d["delta"]
+    for j in range(3, -1, -1):
+        back = back + d["weights"][:, j : j + 1].astype(np.float64) * y[d["pos"][:, j]]
+    assert (back != h).any()  # another order is another sum
