@@ -184,8 +184,10 @@ size_t moe_route_rows_workspace(int32_t T, int32_t local_experts);
  *   after the call; calls in flight at once need one each. Parts of K are
  *   added in FP32, in order; their number depends on R, E, N and K alone.
  * The same call gives the same bits every time. The last FP32 bits of a row's
- * sums may depend on R and on how many rows its expert has, never on what is
- * in other rows or on the row's place among them.
+ * sums may depend on R and E, on how many rows its expert has and, where K is a
+ * multiple of 4096, on the expert's index, so that an expert's rows may differ in
+ * them between calls for all experts and for a share of them; never on what is in
+ * other rows or on the row's place among its expert's.
  * K and N multiples of 128 (N of 256 for the SwiGLU), at most
  * MOE_ROWS_MAX_DIM; E <= 1024; X, R >= 0, at most 2^23 - 9 tiles of work
  * (floor(R/128) + E rows of ceil(N/256) tiles). FP8 and output arrays 16-byte aligned, E8M0

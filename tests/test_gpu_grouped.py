@@ -653,3 +653,40 @@ def test_swiglu_exponential(split):
     act = (g * torch.sigmoid(g) * (xs.double() / 4)).abs()
     assert act.min() > 1e-9
     assert ((s[:, 0].double() * 448.0 - act).abs() <= act * 5 * 2.0**-23).all()
+
+
+@pytest.mark.parametrize("quant", ["fp8", "mxfp8"])
+@pytest.mark.parametrize("counts,N,K", [([3, 0, 17, 40], 256, 2048), ([(7 * e) % 23 for e in range(38)] + [140, 300], 1024, 4096)],
+                         ids=["split", "turned"])
+def test_place_of_a_row_among_its_experts(counts, N, K, quant):
+    """Where K is split, and where tiles begin at blocks of their own: an
+    expert's rows the other way round have the same bits, and so have they beside
+    other experts' other rows."""
+    d = make(counts, N, K, 51, quant, extra=0)
+    n = sum(counts)
+    swiglu = lambda: grouped_swiglu(d["x"], d["x_scale"], d["w"], d["w_scale"], d["offsets"], limit=LIMIT, rows=d["rows"])  # noqa: E731
+    y, (h, s) = call_gemm(d), swiglu()
+    ends = d["offsets"].tolist()
+    d["rows"] = torch.cat([torch.arange(lo, hi).flip(0) for lo, hi in zip(ends, ends[1:])]).int().to(DEV)
+    at = d["rows"].long()
+    y2, (h2, s2) = call_gemm(d), swiglu()
+    assert torch.equal(y2, y[at]) and torch.equal(h2, h[at]) and torch.equal(s2, s[at])
+    last = ends[-2]
+    d["x"][:last] = d["x"][:last].flip(1)
+    y3, (h3, s3) = call_gemm(d), swiglu()
+    assert torch.equal(y3[last:n], y2[last:n]) and torch.equal(h3[last:n], h2[last:n]) and torch.equal(s3[last:n], s2[last:n])
+    assert not torch.equal(y3[:last], y2[:last])
+
+
+def test_a_share_of_the_experts_within_the_bound():
+    """K a multiple of 4096: an expert's rows in a call for a share of the
+    experts may differ in their last FP32 bits, and stay within the bound."""
+    counts = [(7 * e) % 23 for e in range(60)]
+    d = make(counts, 1024, 4096, 52, extra=0)
+    check_gemm_sums(d)
+    lo, hi = 20, 60
+    at = int(d["offsets"][lo])
+    part = dict(d, w=d["w"][lo:hi].contiguous(), w_scale=d["w_scale"][lo:hi].contiguous(), x=d["x"][at:].contiguous(),
+                x_scale=d["x_scale"][at:].contiguous(), offsets=d["offsets"][lo:] - at)
+    check_gemm_sums(part)
+    check_swiglu(part)
