@@ -690,3 +690,39 @@ def test_a_share_of_the_experts_within_the_bound():
                 x_scale=d["x_scale"][at:].contiguous(), offsets=d["offsets"][lo:] - at)
     check_gemm_sums(part)
     check_swiglu(part)
+
+
+@pytest.mark.parametrize("quant", ["fp8", "mxfp8"])
+@pytest.mark.parametrize("counts,N,K", [([3, 0, 17, 140], 384, 2048), ([(7 * e) % 23 for e in range(38)] + [140, 300], 1024, 4096),
+                                        ([40, 100, 170, 230], 384, 1408)], ids=["split", "turned", "heights"])
+def test_exact_integers_of_a_long_k(counts, N, K, quant):
+    """Integers up to 7 and scales of one: sums below 4096 * 49 < 2^18, exact in
+    FP32 in any order, so that one product too many or too few shows."""
+    d = make(counts, N, K, 53, quant, gather=True)
+    gen = torch.Generator(device=DEV).manual_seed(54)
+    d["x"] = torch.randint(-7, 8, d["x"].shape, generator=gen, device=DEV).float().to(F8)
+    d["w"] = torch.randint(-7, 8, d["w"].shape, generator=gen, device=DEV).float().to(F8)
+    d["w_scale"].fill_(1.0)
+    d["x_scale"].fill_(1.0 if quant == "fp8" else 127)
+    want = exact(d)[0].float().to(torch.bfloat16)
+    assert torch.equal(call_gemm(d)[: sum(counts)], want)
+    # no product of eight such codes is 2^14 below another: the FP8 instruction is exact too
+    assert torch.equal(fp8_sums(d)[: sum(counts)], want)
+
+
+@pytest.mark.parametrize("quant", ["fp8", "mxfp8"])
+@pytest.mark.parametrize("counts,N,K", [([70, 3], 1024, 640), ([150, 0, 300], 512, 7168), ([(7 * e) % 23 for e in range(38)] + [140, 300], 1024, 4096)],
+                         ids=["short", "split", "turned"])
+def test_swiglu_sums_in_fp32(counts, N, K, quant):
+    """The hidden's scales on average. up and gate are off by 2^-21 of their
+    root mean square (see check_gemm_sums) and lie above it at a block's maximum;
+    2.1 * 2^-21 and the activation's 5 * 2^-23 are below 2^-19 of the scale."""
+    d = make(counts, N, K, 55, quant, gather=True)
+    if quant == "mxfp8":
+        d["x_scale"].fill_(120)
+    _, s = check_swiglu(d)
+    g, _ = exact(d)
+    n, I = g.shape[0], g.shape[1] // 2
+    act = g[:, I:].clamp_max(LIMIT) * torch.sigmoid(g[:, I:].clamp_max(LIMIT)) * g[:, :I].clamp(-LIMIT, LIMIT)
+    ws = act.abs().view(n, I // 128, 128).amax(-1) / 448.0
+    assert (s[:n].double() / ws - 1.0).square().mean().sqrt() <= 2.0**-19
