@@ -19,17 +19,19 @@
 namespace moe {
 namespace {
 
-template <bool kMx>
+template <bool kMx, bool kAll>
 __global__ __launch_bounds__(kThreads, 2) void grouped_swiglu_kernel(GroupedArgs a) {
   __shared__ Shared sm;
-  grouped_tile<true, kMx>(a, sm);
+  grouped_tile<true, kMx, kAll>(a, sm);
 }
 
 }  // namespace
 
 void launch_grouped_swiglu(bool mx, GroupedArgs a, hipStream_t stream) {
   a.col_tiles = a.N / 256 * a.splits;
-  const auto kernel = mx ? grouped_swiglu_kernel<true> : grouped_swiglu_kernel<false>;
+  const auto kernel = all_of_k(a) ? mx ? grouped_swiglu_kernel<true, true> : grouped_swiglu_kernel<false, true>
+                      : mx        ? grouped_swiglu_kernel<true, false>
+                                  : grouped_swiglu_kernel<false, false>;
   hipLaunchKernelGGL(kernel, dim3(grouped_workgroups(a, a.R, kRows)), dim3(kThreads), 0, stream, a);
 }
 

@@ -332,12 +332,13 @@ __device__ __forceinline__ void any_tile(const GroupedArgs& a, const TileAt& at,
   }
 }
 
-// The whole kernel of a workgroup.
-template <bool kGlu, bool kMx>
+// The whole kernel of a workgroup. kAll: every tile has all of K from its
+// beginning on.
+template <bool kGlu, bool kMx, bool kAll>
 __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, Shared& sm) {
   const TileAt at = find_tile<kRows, kGroup, kThreads>(a, blockIdx.x);
   if (at.e < 0) return;
-  if (whole_k(a, at))
+  if (kAll || whole_k(a, at))
     any_tile<kGlu, kMx, true>(a, at, sm);
   else
     any_tile<kGlu, kMx, false>(a, at, sm);
