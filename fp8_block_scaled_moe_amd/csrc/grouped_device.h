@@ -273,18 +273,21 @@ __device__ __forceinline__ float scale_apart(float s, int byte, int& up) {
   return ldexpf(s, byte - 127 - up);
 }
 
-// gate / (1 + exp(-gate)) * up with both clamped. A clamped NaN stays one. The
-// exponential by the hardware's exp2 of gate log2 e, whose rounding (and that of
-// log2 e) is made up for to first order, so that its error does not grow with
-// |gate|; below -87 a gate counts as -87, whose SiLU is 2^-119.
+// gate / (1 + exp(-gate)) * up with both clamped; a NaN stays one (the median
+// instruction would not keep it). The exponential by the hardware's exp2 of
+// t = -gate log2 e, with what the rounding of t leaves of -gate made up for to
+// first order, so that its error hardly grows with |gate| (by a unit of 2^-23 for
+// 42 of it, that of ln 2); below -87 a gate counts as -87, whose SiLU is 2^-119.
+__device__ __forceinline__ float clamp_nan(float v, float lo, float hi) {
+  return __builtin_elementwise_minimum(__builtin_elementwise_maximum(v, lo), hi);
+}
+
 __device__ __forceinline__ float swiglu(float up, float gate, float limit) {
-  constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
-  up = up != up ? up : __builtin_amdgcn_fmed3f(up, -limit, limit);
-  gate = gate != gate ? gate : __builtin_amdgcn_fmed3f(gate, -87.f, limit);
-  const float t = gate * -kLog2e, rest = fmaf(gate, -kLog2eRest, fmaf(gate, -kLog2e, -t));
-  float e = __builtin_amdgcn_exp2f(t);
-  e = fmaf(e, rest * kLn2, e);
-  return gate * __builtin_amdgcn_rcpf(1.f + e) * up;
+  constexpr float kLog2e = 0x1.715476p+0f, kLn2 = 0x1.62e43p-1f;
+  up = clamp_nan(up, -limit, limit);
+  gate = clamp_nan(gate, -87.f, limit);
+  const float t = gate * -kLog2e, e = __builtin_amdgcn_exp2f(t);
+  return gate * __builtin_amdgcn_rcpf(fmaf(e, fmaf(t, -kLn2, -gate), 1.f + e)) * up;
 }
 
 }  // namespace moe

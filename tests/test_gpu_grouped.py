@@ -633,9 +633,9 @@ def test_e8m0_bytes_from_0_to_230(counts):
 def test_swiglu_exponential(split):
     """One hidden value a row, gate -+x and up x / 4 for a scale x of the row,
     so that the hidden's scale tells it: gates from -20 to 7, none less exact
-    than others. The exponential is within a unit of 2^-23 and a half, 1 + e, the
-    two products and the division by 448 round by a half each and the reciprocal is
-    within a unit: 4.5 units, 5 with their products."""
+    than others. The hardware's exponential and reciprocal are within a unit of
+    2^-23 each, the constant's rounding is another 20 / 42, and 1 + e, its
+    correction, the two products and the division by 448 round by a half each: 5."""
     K = 2048 if split else 128
     R = 4000 if not split else 200
     gen = torch.Generator(device=DEV).manual_seed(50)
