@@ -62,12 +62,21 @@ struct TileAt {
 
 // A workgroup's part of K, in 128-wide blocks, and the block of it that the
 // workgroup begins with (at() wraps round). A tile with all of K from its beginning
-// on (whole_k) has code of its own: the others' costs it 2%. Where K is a multiple of 4096, the
-// blocks of one index of all rows lie in few memory channels, so tiles with
-// weights of their own begin at different blocks. Product, 16 rows for each of
-// 32 experts, N = 2048, without and with it: K = 4096, 64.3 and 45.5 us; 8192, 118 and
-// 86; 12288, 145 and 127. Where K is no such multiple (7168) or row tiles share
-// weights (SwiGLU, 500 rows an expert, K = 8192: 1.17 and 1.20 ms) it costs.
+// on (whole_k) has code of its own: the others' costs it 2%.
+//
+// Where K is a multiple of 4096, the blocks of one index of all rows lie in few
+// memory channels, so tiles with weights of their own (an expert's only row tile)
+// begin at different blocks. Measured with N = 2048, without and with it: 16 rows
+// for each of 32 experts, K = 4096 61 and 43 us, 8192 115 and 80, 12288 160 and 119,
+// 16384 162 and 158; of 64, 120 and 84, 164 and 164, 285 and 243, 323 and 321; of
+// 128, 171 and 174, 331 and 331, 504 and 487; of 15 with K split, 27 and 28, 57 and
+// 45, 66 and 63, 102 and 80. Where K is another multiple of 1024 it costs up to 14%
+// and gains 3 at most (K = 2048, 23 and 26 us; 6144, 64 and 62; 7168, 71 and 72;
+// 10240, 101 and 102). With FP32 sums it pays up to 64 rows in a tile (32 experts:
+// 64 rows, K = 4096 64 and 58 us, 8192 122 and 112; 48 or 64 experts, 8192, up to 9%
+// the other way) and costs 1 to 5% beyond (100 rows, 8192: 157 and 160), where the
+// matrix instructions bind; the FP8 instruction's tiles gain at any height (100
+// rows, K = 8192: 123 and 101 us; 64 experts of 100 rows lose 7%).
 struct KPart {
   int split, first, blocks, start;
   template <bool kWhole>
@@ -75,23 +84,25 @@ struct KPart {
     return kWhole ? b : b + start - (b + start >= blocks ? blocks : 0);
   }
 };
+__device__ __forceinline__ bool turned(const GroupedArgs& a, const TileAt& at, int most_rows) {
+  return at.only && a.K % 4096 == 0 && at.end - at.row <= most_rows;
+}
+__device__ __forceinline__ bool whole_k(const GroupedArgs& a, const TileAt& at, int most_rows) {
+  return a.splits == 1 && !turned(a, at, most_rows);
+}
 // True of every tile: such calls have kernels of their own, since with the other
 // tiles' code beside it the SwiGLU's (8,192 tokens x 8 of 256, K = 7168) took 4.62 ms
 // where it takes 4.58.
 inline bool all_of_k(const GroupedArgs& a) { return a.splits == 1 && a.K % 4096 != 0; }
-__device__ __forceinline__ bool whole_k(const GroupedArgs& a, const TileAt& at) {
-  return a.splits == 1 && !(at.only && a.K % 4096 == 0);
-}
 template <bool kWhole>
-__device__ __forceinline__ KPart k_part(const GroupedArgs& a, const TileAt& at) {
+__device__ __forceinline__ KPart k_part(const GroupedArgs& a, const TileAt& at, int most_rows) {
   if (kWhole) return KPart{0, 0, a.K / 128, 0};
   const int KB = a.K / 128, split = at.col % a.splits;
   const int lo = KB * split / a.splits, n = KB * (split + 1) / a.splits - lo;
   int start = 0;
-  if (at.only && a.K % 4096 == 0) start = (at.e * (a.col_tiles / a.splits) + at.col / a.splits) % n;
+  if (turned(a, at, most_rows)) start = (at.e * (a.col_tiles / a.splits) + at.col / a.splits) % n;
   return KPart{split, lo, n, start};
 }
-
 
 // The workgroup's tile when every expert's rows are cut into as few tiles of
 // at most kRows (a multiple of kGroup) as can be, even but for kGroup rows.

@@ -83,7 +83,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, uin
   const int r16 = lane & 15, g = lane >> 4;
   const int wn = wave & 3, wm = wave >> 2;
   const int first = (groups + 1) / 2, tile_col = kWhole ? at.col : at.col / a.splits;
-  const KPart part = k_part<kWhole>(a, at);
+  const KPart part = k_part<kWhole>(a, at, kRows);
   const int KB = part.blocks;
 
   // What this wave copies of a block: 32 LDS rows of the weights, 4 kJ of the
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_product_fp8_kernel(Groupe
   __shared__ alignas(16) uint8_t shared[kShared];
   const TileAt at = find_tile<kRows, kGroup, kThreads>(a, blockIdx.x);
   if (at.e < 0) return;
-  if (whole_k(a, at))
+  if (whole_k(a, at, kRows))
     any_tile<kMx, true>(a, at, shared);
   else
     any_tile<kMx, false>(a, at, shared);

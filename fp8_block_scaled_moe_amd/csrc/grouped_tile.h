@@ -26,6 +26,7 @@ namespace moe {
 constexpr int kThreads = 512;
 constexpr int kGroup = 32;  // rows of a matrix instruction
 constexpr int kRows = kTileRows;
+constexpr int kTurnRows = 64;  // see KPart
 constexpr int kStages = 3;  // K blocks in LDS: one read, the others on their way
 
 // A K block in LDS, for waves of up to kFirst 32-row groups.
@@ -62,7 +63,7 @@ __device__ __forceinline__ void tile(const GroupedArgs& a, const TileAt& at, Sha
   const int r32 = lane & 31, h = lane >> 5;
   const int wn = wave & 3, wm = wave >> 2;
   const int I = a.N / 2, tile_col = kWhole ? at.col : at.col / a.splits;
-  const KPart part = k_part<kWhole>(a, at);
+  const KPart part = k_part<kWhole>(a, at, kTurnRows);
   const int KB = part.blocks;
 
   // What this wave copies of a block: 32 LDS rows of the weights, 8 kFirst
@@ -338,7 +339,7 @@ template <bool kGlu, bool kMx, bool kAll>
 __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, Shared& sm) {
   const TileAt at = find_tile<kRows, kGroup, kThreads>(a, blockIdx.x);
   if (at.e < 0) return;
-  if (kAll || whole_k(a, at))
+  if (kAll || whole_k(a, at, kTurnRows))
     any_tile<kGlu, kMx, true>(a, at, sm);
   else
     any_tile<kGlu, kMx, false>(a, at, sm);
