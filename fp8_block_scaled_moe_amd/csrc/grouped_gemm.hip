@@ -8,11 +8,12 @@
 // in LDS changes nothing). Where the tiles leave CUs idle, K is split over
 // workgroups, whose FP32 sums go to the workspace and are added here in
 // order (no atomics), before the rounding or the SwiGLU. Without and with it,
-// calls in a graph, one token's 6 experts with 512 columns: product, K = 1024, 8.5
-// and 8.4 us, 2048 13.1 and 8.6, 7168 41.7 and 11.2; SwiGLU 11.3 and 10.6, 17.0 and
-// 11.2, 46.3 and 17.0; 300 tokens x 2 of 8: product, K = 2048, 20.5 and 14.4, 7168
-// 61.0 and 23.9. From Python, where the host needs 4 us for the second launch:
-// K = 1024 10.5 and 14.6, 2048 12.7 and 14.4, 7168 41.3 and 14.4. Parts of at
+// calls in a graph, one token's 6 of 64 experts with 512 columns: product, K = 2048
+// 15.9 and 10.1 us, 7168 44.7 and 12.4; SwiGLU 17.4 and 12.0, 46.6 and 18.0; 300
+// tokens x 2 of 8: product 27.5 and 18.3, 85.4 and 26.0; SwiGLU 29.3 and 23.3, 88.7
+// and 37.5; 1,000 tokens x 2 of 8: 31.7 and 23.8, 98.0 and 38.1, 33.1 and 31.9, 106
+// and 70. K = 1024 takes 9.6 and 11.3 us unsplit and gains nothing in a graph; from
+// Python, where the host needs 4 us for the second launch, it loses them. Parts of at
 // least 2 to 8 blocks were alike.
 #include <hip/hip_runtime.h>
 
@@ -110,7 +111,7 @@ int check(const moe_grouped_args* p) {
   if (misaligned(a.x, 16) || misaligned(a.w, 16) || misaligned(a.out, 16) || misaligned(a.w_scale, 4) ||
       misaligned(a.offsets, 4) || misaligned(a.rows, 4) || misaligned(a.x_scale, 4))
     return MOE_DECODE_ERR_INVALID_ARG;
-  // a grid's limit, 2^32 threads (64-row tiles come with R <= 24 E only, far below it)
+  // a grid's limit, 2^32 threads of 512 a workgroup
   if (((int64_t)a.R / 128 + a.E) * ((a.N + 255) / 256) > (int64_t)(UINT32_MAX / 512) - 8) return MOE_DECODE_ERR_UNSUPPORTED;
   return MOE_DECODE_OK;
 }

@@ -4,14 +4,16 @@
 // would move an FP32 scale by 1e-5, ten times what FP32 sums do.
 //
 // Bounds, measured on MI355X. Few rows: the weights' bytes (4 tokens x 8 of 256
-// experts, K = 7168, I = 2048: 134 us, 6.7 TB/s). Many: the matrix
-// instructions with the 8 vector instructions that each needs (widening, scaled
-// sums), 45% and 48% of the cycles at the 1.8-2.0 GHz that their power allows:
-// 1.0 PFLOP/s for 4,096 rows for each of 8 experts (K = 7168), 1.23 without the
-// copies, 1.3 in a loop of the same instructions on registers; a BF16 library
-// product reaches 1.22. Tiles of 32
-// rows with four blocks in LDS gained 1% below 5 rows an expert and lost 9%
-// at 12, so there is one size.
+// experts, K = 7168, I = 2048: 134 to 140 us, 6.7 TB/s and more). Many: no unit
+// alone. 65,536 rows over 256 such experts take 4.6 ms, 0.83 PFLOP/s: matrix
+// instructions are busy for 44% of the cycles and vector instructions (8.6 for each
+// of them: widening, scaled sums) for 48%, at the 1.8-2.0 GHz that their power
+// allows, and the waves wait for 35% of theirs, since all of a SIMD's are in the same
+// phase of a block between two barriers. Dense rows (4,096 for each of 8 experts)
+// reach 1.0 PFLOP/s, 1.23 without the copies; a loop of the same instructions on
+// registers 1.3, a BF16 library product 1.22. MXFP8 rows 5.1 ms. Tiles of 32 rows with
+// four blocks in LDS gained 1% below 5 rows an expert and lost 9% at 12, so there is
+// one size.
 #include <hip/hip_runtime.h>
 
 #include "grouped_tile.h"

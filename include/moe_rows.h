@@ -179,7 +179,7 @@ size_t moe_route_rows_workspace(int32_t T, int32_t local_experts);
  *   next to a rounding border may differ from that call's.
  * workspace: NULL, or 16-byte aligned device memory of at least
  *   moe_grouped_gemm_workspace / moe_grouped_swiglu_workspace bytes, with which
- *   small calls are split over K, up to 3.7 times faster (SCRATCH_TOO_SMALL
+ *   small calls are split over K, up to 3.6 times faster (SCRATCH_TOO_SMALL
  *   where it is shorter). Its contents need no preparation and mean nothing
  *   after the call; calls in flight at once need one each. Parts of K are
  *   added in FP32, in order; their number depends on R, E, N and K alone.
