@@ -171,12 +171,12 @@ size_t moe_route_rows_workspace(int32_t T, int32_t local_experts);
  * moe_grouped_swiglu: w = W13, N = 2I rows (0..I-1 up, I..2I-1 gate):
  *   up = clamp(g[n], +-limit), gate = min(g[I + n], limit),
  *   act = gate / (1 + exp(-gate)) * up,
- *   out [R, I] e4m3 with out_scale [R, I/128] FP32: MOE_QUANT_FP8 of act.
- *   ("mega_moe" page, hidden_block). act is within (5 + |gate| / 42) * 2^-23 of its
- *   value for the FP32 sums (the hardware's exp2 and reciprocal; a gate below -87
- *   counts as -87), and by the format's definition
- *   multiplied by the reciprocal of its scale, where moe_decode_run divides: a code
- *   next to a rounding border may differ from that call's.
+ *   out [R, I] e4m3 with out_scale [R, I/128] FP32: MOE_QUANT_FP8 of act
+ *   ("mega_moe" page, hidden_block). act is within (5 + |gate| / 42) * 2^-23 of
+ *   its value for the FP32 sums (the hardware's exp2 and reciprocal; a gate below
+ *   -87 counts as -87). By the format's definition it is multiplied by the
+ *   reciprocal of its scale, where moe_decode_run divides: a code next to a
+ *   rounding border may differ from that call's.
  * workspace: NULL, or 16-byte aligned device memory of at least
  *   moe_grouped_gemm_workspace / moe_grouped_swiglu_workspace bytes, with which
  *   small calls are split over K, up to 3.6 times faster (SCRATCH_TOO_SMALL
