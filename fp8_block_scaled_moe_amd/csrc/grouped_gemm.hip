@@ -138,7 +138,7 @@ GroupedArgs kernel_args(const moe_grouped_args& a) {
   g.E = a.E;
   g.N = a.N;
   g.K = a.K;
-  g.limit = a.limit;
+  g.limit = fminf(a.limit, 0x1p127f);  // so that gate log2 e stays finite
   g.splits = a.workspace ? grouped_splits(a.R, a.E, a.N, a.K) : 1;
   g.partial = static_cast<float*>(a.workspace);
   return g;

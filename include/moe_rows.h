@@ -198,7 +198,7 @@ size_t moe_route_rows_workspace(int32_t T, int32_t local_experts);
 typedef struct moe_grouped_args {
   int32_t R, X, E, N, K;
   int32_t quant;     /* of x: MOE_QUANT_FP8, MOE_QUANT_FP8_P2 or MOE_QUANT_MXFP8 */
-  float limit;       /* moe_grouped_swiglu: > 0 */
+  float limit;       /* moe_grouped_swiglu: > 0; above 2^127 it counts as that */
   const void* x;
   const void* x_scale;
   const int32_t* rows;

@@ -726,3 +726,27 @@ def test_swiglu_sums_in_fp32(counts, N, K, quant):
     act = g[:, I:].clamp_max(LIMIT) * torch.sigmoid(g[:, I:].clamp_max(LIMIT)) * g[:, :I].clamp(-LIMIT, LIMIT)
     ws = act.abs().view(n, I // 128, 128).amax(-1) / 448.0
     assert (s[:n].double() / ws - 1.0).square().mean().sqrt() <= 2.0**-19
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_swiglu_without_a_limit(split):
+    """limit = infinity: ordinary values as with a limit above them, and gates up
+    to the largest value give no NaN."""
+    K = 2048 if split else 256
+    d = make([5, 40], 256, K, 56, extra=0)
+    call = lambda limit: grouped_swiglu(d["x"], d["x_scale"], d["w"], d["w_scale"], d["offsets"], limit=limit)  # noqa: E731
+    (h, s), (h2, s2) = call(float("inf")), call(1e30)
+    assert torch.equal(h, h2) and torch.equal(s, s2)
+    one = torch.zeros(45, K, device=DEV)
+    one[:, 3], one[:, 130] = 1.0, 1.0
+    d["x"], d["w"] = one.to(F8), torch.zeros_like(d["w"].float()).to(F8)
+    d["w"][:, 9, 130], d["w"][:, 128 + 9, 3] = 1.0, 1.0  # up of the second block's scale, gate of the first's
+    d["x_scale"].fill_(2.0**-60)
+    gate = torch.linspace(1e38, 3.4e38, 45, device=DEV)
+    gate[0] = 50.0
+    d["x_scale"][:, 0] = gate
+    d["w_scale"].fill_(1.0)
+    h, s = call(float("inf"))
+    act = gate.double().clamp_max(2.0**127) * 2.0**-60
+    assert ((s[:, 0].double() * 448.0 / act.clamp_min(1e-10) - 1.0).abs() < 2.0**-20).all()
+    assert (h.view(F8)[1:, 9].float() == 448.0).all() and not h[1:, :9].any() and not h[1:, 10:].any()
