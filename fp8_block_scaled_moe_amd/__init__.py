@@ -1,10 +1,15 @@
 """Routed-expert FP8 block-scaled MoE decode for MI355X (gfx950).
 
 The compute path is the HIP library libmoe_decode.so (C ABI in
-include/moe_decode.h, include/moe_boundary.h and include/moe_rows.h); this
-package is its thin Python binding. Build the library with `python -m fp8_block_scaled_moe_amd.build`.
+include/moe_decode.h, include/moe_boundary.h, include/moe_rows.h and
+include/moe_block.h); this package is its thin Python binding. Build the library with `python -m fp8_block_scaled_moe_amd.build`.
 """
 
+from ._block import (  # noqa: F401
+    dense_gemm,
+    join_rmsnorm_quant,
+    route_rows_scored,
+)
 from ._capi import (  # noqa: F401
     MoeDecode,
     MoeDecodeConfig,

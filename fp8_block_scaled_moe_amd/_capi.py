@@ -134,7 +134,8 @@ def lib() -> ctypes.CDLL:
     L.moe_mxfp8_quantize.restype = ctypes.c_int
     L.moe_reduce_rmsnorm.argtypes = [vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, vp]
     L.moe_reduce_rmsnorm.restype = ctypes.c_int
-    for name in ("moe_add_rmsnorm_quant", "moe_route_rows", "moe_grouped_gemm", "moe_grouped_swiglu"):
+    for name in ("moe_add_rmsnorm_quant", "moe_route_rows", "moe_grouped_gemm", "moe_grouped_swiglu",
+                 "moe_dense_gemm", "moe_route_rows_scored", "moe_join_rmsnorm_quant"):
         getattr(L, name).argtypes = [vp, vp]
         getattr(L, name).restype = ctypes.c_int
     L.moe_route_rows_workspace.argtypes = [i32, i32]
@@ -142,6 +143,8 @@ def lib() -> ctypes.CDLL:
     for name in ("moe_grouped_gemm_workspace", "moe_grouped_swiglu_workspace"):
         getattr(L, name).argtypes = [i32, i32, i32, i32]
         getattr(L, name).restype = sz
+    L.moe_dense_gemm_workspace.argtypes = [i32, i32, i32]
+    L.moe_dense_gemm_workspace.restype = sz
     _lib = L
     return L
 

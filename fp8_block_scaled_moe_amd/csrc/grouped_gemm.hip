@@ -96,8 +96,6 @@ size_t workspace(int R, int E, int N, int K) {
   return splits > 1 ? (size_t)splits * R * N * sizeof(float) : 0;
 }
 
-bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
-
 int check(const moe_grouped_args* p) {
   if (!p) return MOE_DECODE_ERR_INVALID_ARG;
   const moe_grouped_args& a = *p;

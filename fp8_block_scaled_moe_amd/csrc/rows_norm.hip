@@ -20,68 +20,8 @@
 namespace moe {
 namespace {
 
-constexpr int kVec = 8;        // columns per lane and chunk (16 bytes of BF16)
-constexpr int kBatch = 8;      // expert rows requested before they are added
-constexpr int kMaxPicks = 32;
+constexpr int kBatch = 8;  // expert rows requested before they are added
 constexpr int kFewTokens = 512;  // see the launch
-
-__device__ __forceinline__ void unpack8(const u32x4_t& w, float (&v)[kVec]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_value(w[i] & 0xFFFFu);
-    v[2 * i + 1] = bf16_value(w[i] >> 16);
-  }
-}
-
-__device__ __forceinline__ u32x4_t pack8(const float (&v)[kVec]) {
-  return u32x4_t{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7])};
-}
-
-__device__ __forceinline__ u32x4_t load16(const void* p, size_t at) {
-  return *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + at);
-}
-
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) v += __shfl_xor(v, o, kWave);
-  return v;
-}
-
-// The 8-bit form of a lane's eight values of row t from column col on; the
-// lanes of a block (16 for 128 values, 4 for 32) hold neighbouring columns.
-// Lanes past the row (live false) take part in the permutations only.
-__device__ __forceinline__ void store_quant(const moe_norm_args& a, const float (&v)[kVec], int t, int col, bool live) {
-  float amax = a.quant == MOE_QUANT_MXFP8 ? 0.f : kAmaxFloor;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) amax = fmaxf(amax, fabsf(v[i]));
-  u32x2_t codes;
-  if (a.quant == MOE_QUANT_MXFP8) {
-    amax = dpp_max4(amax);
-    const uint32_t u = __float_as_uint(amax);
-    int shared = -127;
-    if (u) shared = (u >> 23) ? (int)(u >> 23) - 127 - 8 : 31 - __builtin_clz(u) - 149 - 8;
-    shared = max(shared, -127);
-    float w[kVec];
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) w[i] = ldexpf(v[i], -shared);
-    codes[0] = e4m3x4_encode_nan(w[0], w[1], w[2], w[3]);
-    codes[1] = e4m3x4_encode_nan(w[4], w[5], w[6], w[7]);
-    if (live && (threadIdx.x & 3) == 0)
-      static_cast<uint8_t*>(a.scale)[(size_t)t * (a.D / 32) + col / 32] = (uint8_t)(shared + 127);
-  } else {
-    amax = dpp_max16(amax);
-    float s = amax / kFp8Max;
-    if (a.quant == MOE_QUANT_FP8_P2) {
-      const uint32_t b = __float_as_uint(fmaxf(s, kAmaxFloor));
-      s = __uint_as_float(((b >> 23) + ((b & 0x7FFFFFu) != 0u)) << 23);
-    }
-    const float inv = 1.0f / s;
-    codes[0] = e4m3x4_encode_nan(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-    codes[1] = e4m3x4_encode_nan(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
-    if (live && (threadIdx.x & 15) == 0) static_cast<float*>(a.scale)[(size_t)t * (a.D / 128) + col / 128] = s;
-  }
-  if (live) *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(a.q) + (size_t)t * a.D + col) = codes;
-}
 
 template <int kChunks, bool kRouted>
 __global__ __launch_bounds__(1024) void norm_kernel(moe_norm_args a) {
@@ -181,8 +121,6 @@ void launch_norm(const moe_norm_args& a, int threads, hipStream_t stream) {
     hipLaunchKernelGGL((norm_kernel<kChunks, false>), dim3(a.T), dim3(threads), 0, stream, a);
 }
 
-bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
-
 }  // namespace
 }  // namespace moe
 
@@ -190,23 +128,8 @@ extern "C" int moe_add_rmsnorm_quant(const moe_norm_args* args, void* stream) {
   using namespace moe;
   if (!args) return MOE_DECODE_ERR_INVALID_ARG;
   const moe_norm_args& a = *args;
-  if (a.T == 0) return MOE_DECODE_OK;
-  if (a.T < 0 || a.R < 0 || a.k < 0 || !(a.eps >= 0.f) || !(a.eps <= 3.4e38f)) return MOE_DECODE_ERR_INVALID_ARG;
-  if (a.quant < MOE_QUANT_NONE || a.quant > MOE_QUANT_MXFP8 || a.k > kMaxPicks || a.T > MOE_ROWS_MAX_TOKENS)
-    return MOE_DECODE_ERR_UNSUPPORTED;
-  const int unit = a.quant == MOE_QUANT_NONE ? kVec : a.quant == MOE_QUANT_MXFP8 ? 32 : 128;
-  if (a.D <= 0 || a.D % unit || a.D > MOE_ROWS_MAX_D) return MOE_DECODE_ERR_UNSUPPORTED;
-  if (!a.residual && !a.delta && !a.y) return MOE_DECODE_ERR_INVALID_ARG;
-  if (!a.residual_out && !a.out && !a.q) return MOE_DECODE_ERR_INVALID_ARG;
-  const bool routed = a.k > 0;
-  if (routed != (a.y != nullptr) || routed != (a.pos != nullptr) || routed != (a.weights != nullptr))
-    return MOE_DECODE_ERR_INVALID_ARG;
-  const bool quant = a.quant != MOE_QUANT_NONE;
-  if (quant != (a.q != nullptr) || quant != (a.scale != nullptr)) return MOE_DECODE_ERR_INVALID_ARG;
-  if (misaligned(a.residual, 16) || misaligned(a.delta, 16) || misaligned(a.y, 16) || misaligned(a.gamma, 16) ||
-      misaligned(a.residual_out, 16) || misaligned(a.out, 16) || misaligned(a.q, 16) || misaligned(a.pos, 4) ||
-      misaligned(a.weights, 4) || (a.quant != MOE_QUANT_MXFP8 && misaligned(a.scale, 4)))
-    return MOE_DECODE_ERR_INVALID_ARG;
+  const int rc = check_norm(a);
+  if (rc != MOE_DECODE_OK || a.T == 0) return rc;
   // Lanes for one chunk each: many, with all of a row's loads on their way at
   // once, for routed rows (whose positions come first: 4,096 tokens of eight
   // rows of 7168, 150 us against 171) and for few tokens (7168 columns: one
@@ -216,7 +139,7 @@ extern "C" int moe_add_rmsnorm_quant(const moe_norm_args* args, void* stream) {
   const int lanes = a.D / kVec;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const auto waves = [](int n) { return (n + kWave - 1) / kWave * kWave; };
-  const bool wide = routed || a.T <= kFewTokens;
+  const bool wide = a.k > 0 || a.T <= kFewTokens;
   if (lanes <= (wide ? 1024 : 256))
     launch_norm<1>(a, waves(lanes), s);
   else if (wide || lanes <= 512)
