@@ -23,6 +23,7 @@ ACTS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5}
 SCORES = {"sigmoid": 0, "softmax": 1}
 GATE_NONE, GATE_ROW, GATE_COLUMN, GATE_FULL = range(4)
 DENSE_MAX_DIM = 1048576
+DENSE_MAX_STRIDE = 2**23  # of rows of x, w and the residual, in values
 ROUTE_MAX_GROUPS = 64
 
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
@@ -63,6 +64,8 @@ def _matrix(t, name, dtypes, dev, shape, unit):
         raise ValueError(f"the rows of {name} must be contiguous")
     if rows > 1 and (ld < columns or ld % unit):
         raise ValueError(f"the rows of {name} must not overlap and lie a multiple of {unit} values apart, got {ld}")
+    if rows > 1 and ld >= DENSE_MAX_STRIDE:
+        raise ValueError(f"the rows of {name} must lie less than 2^23 values apart, got {ld}")
     p = t.data_ptr()
     align = 16 if unit > 1 else t.element_size()
     if p % align:

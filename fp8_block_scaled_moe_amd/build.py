@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_decode.so")
 SOURCES = ["capi.hip", "route_quant.hip", "expert_gemm.hip", "expert_gemm_wg.hip", "expert_gemm_fp4.hip", "epilogues.hip",
            "boundary.hip", "rows_norm.hip", "rows_route.hip", "grouped_gemm.hip", "grouped_product.hip",
-           "grouped_product_fp8.hip", "grouped_swiglu.hip", "dense_gemm.hip", "dense_strip.hip", "rows_scored.hip", "rows_join.hip"]
+           "grouped_product_fp8.hip", "grouped_swiglu.hip", "dense_gemm.hip", "dense_strip.hip", "dense_tile.hip", "rows_scored.hip", "rows_join.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -5,7 +5,9 @@
 // As rows_norm.hip: one workgroup per token holds the whole row in registers, eight
 // columns a lane and chunk, so every input is read once and every output written once.
 // The second norm's statistics need the first's, so a row crosses the workgroup
-// twice; both sums of squares are taken in FP64.
+// twice; both sums of squares are taken in FP64, and the normalised and gated row
+// stays in FP64 up to its sum with the residual: three roundings less on the way to
+// the 8-bit codes than with FP32 products, for two FP64 products a value.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -19,18 +21,18 @@ namespace {
 constexpr int kBatch = 8;  // expert rows requested before they are added
 constexpr int kFewTokens = 512;  // see the launch
 
-// FP32(1 / sqrt(mean + eps)) of a sum of squares over the workgroup. Barrier inside.
-__device__ __forceinline__ float row_rstd(double sq, double* part, int D, float eps) {
+// 1 / sqrt(mean + eps) of a sum of squares over the workgroup. Barrier inside.
+__device__ __forceinline__ double row_rstd(double sq, double* part, int D, float eps) {
   sq = wave_sum_f64(sq);
   if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = sq;
   __syncthreads();
   double total = 0.0;
   for (int w = 0; w < (int)blockDim.x / kWave; ++w) total += part[w];
-  return (float)(1.0 / sqrt(total / (double)D + (double)eps));
+  return 1.0 / sqrt(total / (double)D + (double)eps);
 }
 
 template <int kChunks, bool kRouted>
-__global__ __launch_bounds__(1024) void join_kernel(moe_join_args ja) {
+__global__ __launch_bounds__(kChunks == 4 ? 512 : 1024) void join_kernel(moe_join_args ja) {
   __shared__ double part[2][16];
   const moe_norm_args& a = ja.norm;
   const int t = blockIdx.x, tid = threadIdx.x;
@@ -96,35 +98,28 @@ __global__ __launch_bounds__(1024) void join_kernel(moe_join_args ja) {
       sq = fma((double)h[c][i], (double)h[c][i], sq);
     }
   }
-  if (ja.post_gamma) {
-    const float rstd = row_rstd(sq, part[0], a.D, ja.post_eps);
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      float pv[kVec];
-      unpack8(p[c], pv);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) h[c][i] = (h[c][i] * rstd) * (pv[i] + ja.gamma_offset);
-    }
-  }
+  const double rstd_post = ja.post_gamma ? row_rstd(sq, part[0], a.D, ja.post_eps) : 1.0;
   sq = 0.0;
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
     const int col = (c * (int)blockDim.x + tid) * kVec;
     const bool live = col < a.D;
-    float rv[kVec], uv[kVec];
+    float rv[kVec], uv[kVec], pv[kVec];
     unpack8(r[c], rv);
     unpack8(u[c], uv);
+    unpack8(p[c], pv);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const double by = ja.gate_kind >= MOE_GATE_COLUMN ? (double)uv[i] : gate;
-      const float v = (float)fma((double)h[c][i], by, (double)rv[i] * (double)ja.residual_scale);  // both products are exact
+      double by = ja.gate_kind >= MOE_GATE_COLUMN ? (double)uv[i] : gate;
+      if (ja.post_gamma) by *= rstd_post * (double)(pv[i] + ja.gamma_offset);
+      const float v = (float)fma((double)h[c][i], by, (double)rv[i] * (double)ja.residual_scale);
       h[c][i] = live ? v : 0.f;
       sq = fma((double)h[c][i], (double)h[c][i], sq);
     }
     if (a.residual_out && live) *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.residual_out) + row + col) = pack8(h[c]);
   }
   if (a.gamma) {
-    const float rstd = row_rstd(sq, part[1], a.D, a.eps);
+    const float rstd = (float)row_rstd(sq, part[1], a.D, a.eps);
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       float gv[kVec];

@@ -66,7 +66,8 @@ extern "C" {
  *   contents need no preparation and mean nothing after the call; calls in
  *   flight at once need one each.
  * K a multiple of 8; N and K from 1 (8) to MOE_DENSE_MAX_DIM; 0 <= T <=
- * MOE_ROWS_MAX_TOKENS; ldx and ldw multiples of 8, at least K, ldr at least N;
+ * MOE_ROWS_MAX_TOKENS; ldx and ldw multiples of 8, at least K, ldr at least N, all
+ * below 2^23;
  * rows of x, w 16-byte aligned, bias, residual to their element, out 16 bytes.
  * Strides of a tensor with a single row are not read. T = 0 is a valid empty
  * call. */
@@ -134,16 +135,16 @@ int moe_route_rows_scored(const moe_route_scored_args* a, void* stream);
  *   b = delta[t] + sum_j weights[t, j] * y[pos[t, j]]
  *       summed in FP64 in this order and rounded to FP32 (a position outside
  *       [0, R) adds nothing);
- *   n = (b * rstd(b)) * (post_gamma + gamma_offset), or b without post_gamma,
- *       rstd(b) = FP32(1 / sqrt(sum_i b_i^2 / D + post_eps));
- *   h = FP32(residual_scale * residual[t] + gate * n), the sum in FP64;
- *   v = (h * rstd(h)) * (gamma + gamma_offset), or h without gamma, with eps;
+ *   n = b * rstd(b) * (post_gamma + gamma_offset), or b without post_gamma,
+ *       rstd(b) = 1 / sqrt(sum_i b_i^2 / D + post_eps), in FP64 but for the FP32
+ *       addition of gamma_offset;
+ *   h = residual_scale * residual[t] + gate * n, in FP64, rounded to FP32 once;
+ *   v = (h * FP32(rstd(h))) * (gamma + gamma_offset) in FP32, or h without gamma,
+ *       with eps, the statistics in FP64;
  *   residual_out[t] = BF16(h), out[t] = BF16(v), q[t] and scale[t] = the 8-bit
  *   form of v (not of BF16(v)).
- * The products of n and v and the additions of gamma_offset are rounded to FP32
- * each, statistics are taken in FP64; T and k choose the order of their sums,
- * which may move the last bit of an rstd next to a rounding border; the same
- * call gives the same bits.
+ * T and k choose the order of the statistics' sums, which may move the last bit of
+ * a value next to a rounding border; the same call gives the same bits.
  *   norm   sizes, quantisation and arrays as in moe_add_rmsnorm_quant;
  *          residual may be NULL (0), delta and the routed rows not both;
  *          residual_out may be `residual` or `delta` itself

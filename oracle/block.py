@@ -87,21 +87,20 @@ def route_scored(logits, bias, top_k: int, routed_scale: float, *, kind: str = "
     return ids, weights, key
 
 
-def _rms(h, gamma, eps, offset):
-    h = np.asarray(h, np.float64)
-    rstd = f32(1.0 / np.sqrt((h * h).mean(axis=1, keepdims=True) + float(f32(eps))))
-    return f32(f32(h * rstd) * f32(np.asarray(gamma, np.float64) + float(f32(offset))))
+def _rstd(h, eps):
+    return 1.0 / np.sqrt((h * h).mean(axis=1, keepdims=True) + float(f32(eps)))
 
 
 def join_rows(residual, delta, y, pos, weights, *, gamma, eps, post_gamma=None, post_eps=None, gate=None, residual_scale=1.0,
               gamma_offset=0.0):
-    """(h, v): the residual row and its normalised form, binary32 values; gate
-    broadcasts against [T, D]."""
-    b = sum_rows(None, delta, y, pos, weights)
+    """(h, v): the residual row, float64 up to its one rounding, and its
+    normalised form, binary32 values; gate broadcasts against [T, D]."""
+    b = np.asarray(sum_rows(None, delta, y, pos, weights), np.float64)
+    plus = lambda g: np.asarray(f32(np.asarray(g, np.float64) + float(f32(gamma_offset))), np.float64)  # noqa: E731
     if post_gamma is not None:
-        b = _rms(b, post_gamma, eps if post_eps is None else post_eps, gamma_offset)
-    h = np.asarray(b, np.float64) * (1.0 if gate is None else np.asarray(gate, np.float64))
+        b = b * _rstd(b, eps if post_eps is None else post_eps) * plus(post_gamma)
+    h = b * (1.0 if gate is None else np.asarray(gate, np.float64))
     if residual is not None:
         h = h + np.asarray(residual, np.float64) * float(f32(residual_scale))
-    h = f32(h)
-    return h, h if gamma is None else _rms(h, gamma, eps, gamma_offset)
+    h = np.asarray(f32(h), np.float64)
+    return h, h if gamma is None else f32(f32(h * f32(_rstd(h, eps))) * plus(gamma))

@@ -82,6 +82,39 @@ def test_sizes(T, N, K):
     check(make(T, N, K, T + N + K + 2, bias=torch.float32, residual=torch.float32), dtype=torch.float32)
 
 
+# tiles of every size, whole and ragged rounds of them, K split over workgroups, rows that begin anywhere
+LARGE = [(138, 3584, 7168), (200, 4096, 7160), (256, 4096, 7168), (256, 4093, 7168), (200, 4001, 6000), (350, 4090, 648), (363, 896, 7168),
+         (300, 7168, 2048), (311, 7165, 520), (900, 7100, 328), (1900, 1000, 2056), (2300, 3000, 72), (3000, 7000, 136), (4200, 4600, 136),
+         (4352, 4096, 72), (4500, 2600, 520), (4500, 2601, 1032), (5000, 2000, 1032), (6000, 2600, 520), (8192, 2048, 128), (8191, 896, 3584),
+         (9078, 256, 1024), (10807, 1, 2472), (16384, 30, 64), (3, 8192, 8192), (64, 8191, 4096)]
+
+
+def exact_on_gpu(d, act):
+    """The same in FP64 on the GPU, and the bound."""
+    x, w = d["x"].double(), d["w"].double()
+    before = x @ w.t()
+    mag = x.abs() @ w.abs().t()
+    if d.get("bias") is not None:
+        before = before + d["bias"].double()
+    out = {None: lambda v: v, "relu": lambda v: v.clamp_min(0), "silu": lambda v: v / (1 + (-v).exp()),
+           "gelu": lambda v: 0.5 * v * (1 + torch.erf(v * 0.5**0.5))}[act](before)
+    res = d["residual"].double() if d.get("residual") is not None else torch.zeros_like(out)
+    err = 1.13 * (x.shape[1] / 16 + 64) * 2.0**-23 * mag + 8 * 2.0**-23 * (before.abs() + out.abs() + 2 * res.abs() + 1.0 + 8.0)
+    return out + res, err
+
+
+@pytest.mark.parametrize("T,N,K", LARGE)
+def test_large_sizes(T, N, K):
+    for act, dtype, bias, residual in ((None, BF, None, None), ("silu", torch.float32, torch.float32, BF), ("gelu", BF, BF, torch.float32),
+                                       ("relu", torch.float32, None, torch.float32)):
+        d = make(T, N, K, T + K, bias=bias, residual=residual)
+        got = dense_gemm(**d, act=act, out_dtype=dtype).double()
+        out, err = exact_on_gpu(d, act)
+        err = err + (out.abs() + err) * torch.finfo(dtype).eps / 2
+        off = (got - out).abs()
+        assert bool((off <= err).all()), f"{act} {dtype}: {int((off > err).sum())} values outside, the worst {float((off / err).max())} times"
+
+
 @pytest.mark.parametrize("seed", range(40))
 def test_drawn_sizes(seed):
     rng = np.random.default_rng(seed)
@@ -181,7 +214,7 @@ def test_relu_keeps_a_nan():
     assert got[1].isnan().all() and (got[0] == 8).all()
 
 
-@pytest.mark.parametrize("T,N,K", [(1, 256, 7168), (33, 200, 4096), (509, 512, 7168), (700, 768, 512)])
+@pytest.mark.parametrize("T,N,K", [(1, 256, 7168), (33, 200, 4096), (256, 4096, 7168), (509, 512, 7168), (700, 768, 512), (4500, 2600, 264)])
 def test_same_bits_and_rows_alone(T, N, K):
     """A call gives the same bits again, and a row's do not depend on the others' values."""
     d = make(T, N, K, 17, bias=BF)
@@ -202,7 +235,8 @@ def raw(d, out, workspace=None, nbytes=0, T=None, **over):
     return lib().moe_dense_gemm(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
 
 
-@pytest.mark.parametrize("T,N,K", [(1, 30, 64), (13, 33, 136), (100, 130, 1024), (257, 264, 512), (509, 300, 2048)])
+@pytest.mark.parametrize("T,N,K", [(1, 30, 64), (13, 33, 136), (100, 130, 1024), (257, 264, 512), (509, 300, 2048), (256, 4091, 7168),
+                                   (256, 4096, 7168), (3000, 2603, 72), (4500, 2600, 264)])
 @pytest.mark.parametrize("dtype", [BF, torch.float32])
 def test_nothing_behind_the_output_is_written(T, N, K, dtype):
     d = make(T, N, K, 19)
@@ -214,14 +248,14 @@ def test_nothing_behind_the_output_is_written(T, N, K, dtype):
     assert torch.equal(out[: T * N].view(T, N), dense_gemm(**d, out_dtype=dtype))
 
 
-@pytest.mark.parametrize("T,N,K", [(1, 256, 7168), (200, 256, 7168), (509, 512, 7168)])
+@pytest.mark.parametrize("T,N,K", [(1, 256, 7168), (200, 256, 7168), (256, 4096, 7168)])
 def test_without_a_workspace(T, N, K):
     """The product is right without one, too."""
     d = make(T, N, K, 23)
     out = torch.empty(T, N, dtype=torch.float32, device=DEV)
     assert raw(d, out) == _capi.OK
-    exact = host(d["x"]) @ host(d["w"]).T
-    assert (np.abs(host(out) - exact) <= bound(d, K, None, exact, exact, torch.float32)).all()
+    exact, err = exact_on_gpu(d, None)
+    assert bool(((out.double() - exact).abs() <= err).all())
 
 
 def test_empty_and_single_rows():
@@ -233,7 +267,7 @@ def test_empty_and_single_rows():
     check(dict(x=x, w=w, residual=torch.randn(1, 1, device=DEV)))
 
 
-@pytest.mark.parametrize("T,N,K", [(1, 256, 7168), (130, 256, 4096), (600, 1024, 512)])
+@pytest.mark.parametrize("T,N,K", [(1, 256, 7168), (130, 256, 4096), (256, 4096, 7168), (600, 1024, 512)])
 def test_captured_and_replayed(T, N, K):
     """Two calls in one graph, replayed with eager work between, new inputs each time."""
     d = make(T, N, K, 29, bias=BF)
@@ -259,7 +293,8 @@ def test_captured_and_replayed(T, N, K):
 
 def test_two_streams_and_a_given_stream():
     """Calls in flight at once have workspaces of their own."""
-    a, b = make(130, 256, 4096, 31), make(130, 256, 4096, 32)
+    a, b = make(256, 4096, 7168, 31), make(256, 4096, 7168, 32)
+    assert lib().moe_dense_gemm_workspace(256, 4096, 7168)
     wa, wb = dense_gemm(**a), dense_gemm(**b)
     torch.cuda.synchronize()
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
@@ -273,18 +308,18 @@ def test_two_streams_and_a_given_stream():
 
 
 def test_offsets_past_32_bits():
-    """Rows of x 2^31 values apart, of the residual likewise, outputs past 2^31 values."""
-    K, N, T, ld = 64, 24, 3, 2**31
-    big = torch.empty(2 * ld + 4096, dtype=BF, device=DEV)
-    x = big.as_strided((T, K), (ld, 1))
-    r = big.as_strided((T, N), (ld, 1), 1024)
-    x.normal_()
-    r.normal_()
-    w = torch.randn(N, K, device=DEV).to(BF)
-    check(dict(x=x, w=w, residual=r))
-    wide = big.as_strided((3, K), (ld, 1), 2048)
-    wide.normal_()
-    check(dict(x=torch.randn(5, K, device=DEV).to(BF), w=wide))
+    """Rows 2^23 - 8 values apart, the largest stride, so that offsets of x, w and the
+    residual pass 2^32 values; outputs past 2^31 values."""
+    K, N, T, ld = 64, 24, 600, 2**23 - 8
+    big = torch.empty(T * ld, dtype=BF, device=DEV)
+    x, r, w = big.as_strided((T, K), (ld, 1)), big.as_strided((T, N), (ld, 1), 1024), big.as_strided((T, K), (ld, 1), 2048)
+    for t in (x, r, w):
+        t.normal_()
+    assert T * ld > 2**32
+    check(dict(x=x, w=torch.randn(N, K, device=DEV).to(BF), residual=r))
+    check(dict(x=torch.randn(5, K, device=DEV).to(BF), w=w))
+    check(dict(x=x, w=w))
+    wide = w
     del big, x, r, wide
     T, N = 300000, 7200
     x, w = torch.randn(T, 8, device=DEV).to(BF), torch.randn(N, 8, device=DEV).to(BF)
