@@ -2,11 +2,15 @@
 // activations and the epilogue.
 #pragma once
 
+#include <type_traits>
+
 #include "../../include/moe_block.h"
 #include "grouped_device.h"
 #include "rows_device.h"
 
 namespace moe {
+
+constexpr int kCus = 256;
 
 // Rows at most this far apart, so that the 256 rows of a tile lie within 2^32 bytes.
 constexpr int64_t kDenseMaxStride = (1 << 23) - 1;
@@ -29,31 +33,62 @@ struct DenseArgs {
 // Columns of a row of partial sums: whole groups of eight.
 __host__ __device__ inline size_t dense_pitch(int N) { return ((size_t)N + 7) / 8 * 8; }
 
-// 1 / (1 + exp(-v)) times u. The exponential by the hardware's exp2 of t =
-// -v log2 e, with what the rounding of t leaves of -v made up for to first order, so
-// that its error hardly grows with |v|. Below -87 v counts as -87 (the value is 2^-125
-// then); a NaN stays one.
+// 1 / (1 + exp(-v)) times u, from t = -v log2 e by the hardware's exp2 and reciprocal.
+// kFine (FP32 outputs): what the rounding of t leaves of -v is made up for to first
+// order, so that the error hardly grows with |v|, which counts as -87 below that (the
+// value is 2^-125 then). For BF16 outputs without: |v| 2^-23 of the value and less, a
+// thousandth of their step, for two thirds of the cycles. A NaN stays one.
+template <bool kFine>
 __device__ __forceinline__ float times_sigmoid(float v, float u) {
   constexpr float kLog2e = 0x1.715476p+0f, kLn2 = 0x1.62e43p-1f;
+  if (!kFine) return u * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -kLog2e));
   v = clamp_nan(v, -87.f, 3.0e38f);
   const float t = v * -kLog2e, e = __builtin_amdgcn_exp2f(t);
   return u * __builtin_amdgcn_rcpf(fmaf(e, fmaf(t, -kLn2, -v), 1.f + e));
 }
 
-__device__ __forceinline__ float activation(float v, int act) {
-  switch (act) {
+template <int kAct, bool kFine>
+__device__ __forceinline__ float activation(float v) {
+  switch (kAct) {
     case MOE_ACT_RELU:
       return __builtin_elementwise_maximum(v, 0.f);
     case MOE_ACT_SILU:
-      return times_sigmoid(v, v);
+      return times_sigmoid<kFine>(v, v);
     case MOE_ACT_GELU:
       return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
     case MOE_ACT_GELU_TANH:  // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
-      return times_sigmoid(v * fmaf(v * v, 0.0713548162726009f, 1.5957691216057308f), v);
+      return times_sigmoid<kFine>(v * fmaf(v * v, 0.0713548162726009f, 1.5957691216057308f), v);
     case MOE_ACT_SIGMOID:
-      return times_sigmoid(v, 1.f);
+      return times_sigmoid<kFine>(v, 1.f);
     default:
       return v;
+  }
+}
+
+// One activation for all of v: the choice stands outside of the values.
+template <int kN>
+__device__ __forceinline__ void activate(const DenseArgs& a, float (&v)[kN]) {
+  const auto all = [&](auto act, auto fine) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = activation<decltype(act)::value, decltype(fine)::value>(v[i]);
+  };
+  const auto either = [&](auto act) {
+    if (a.out_f32)
+      all(act, std::true_type{});
+    else
+      all(act, std::false_type{});
+  };
+  switch (a.act) {
+    case MOE_ACT_RELU:
+      return all(std::integral_constant<int, MOE_ACT_RELU>{}, std::true_type{});
+    case MOE_ACT_SILU:
+      return either(std::integral_constant<int, MOE_ACT_SILU>{});
+    case MOE_ACT_GELU:
+      return all(std::integral_constant<int, MOE_ACT_GELU>{}, std::true_type{});
+    case MOE_ACT_GELU_TANH:
+      return either(std::integral_constant<int, MOE_ACT_GELU_TANH>{});
+    case MOE_ACT_SIGMOID:
+      return either(std::integral_constant<int, MOE_ACT_SIGMOID>{});
   }
 }
 
@@ -64,7 +99,9 @@ __device__ __forceinline__ float element(const void* p, size_t i, bool f32) {
 // Bias, activation and residual of one value, and its store.
 __device__ __forceinline__ void finish(const DenseArgs& a, int t, int n, float v) {
   if (a.bias) v += element(a.bias, n, a.bias_f32);
-  v = activation(v, a.act);
+  float one[1] = {v};
+  activate(a, one);
+  v = one[0];
   if (a.residual) v += element(a.residual, (size_t)t * a.ldr + n, a.residual_f32);
   const size_t o = (size_t)t * a.N + n;
   if (a.out_f32)
@@ -73,7 +110,8 @@ __device__ __forceinline__ void finish(const DenseArgs& a, int t, int n, float v
     static_cast<uint16_t*>(a.out)[o] = (uint16_t)bf16x2_bits(v, 0.f);
 }
 
-// Eight neighbouring columns from n on: their bias, and how a row's sums of them end.
+// Eight neighbouring columns from n on: their bias, and how kRows rows' sums of them end.
+template <int kRows>
 struct Columns {
   int n, count;  // columns below N
   float bias[8];
@@ -81,64 +119,58 @@ struct Columns {
 #pragma unroll
     for (int i = 0; i < 8; ++i) bias[i] = a.bias && i < count ? element(a.bias, n + i, a.bias_f32) : 0.f;
   }
-  // Row t's sums (of part `split` of K where there are several).
-  __device__ __forceinline__ void finish(const DenseArgs& a, int t, int split, const float4_t& lo, const float4_t& hi) const {
-    if (a.splits > 1) {
-      float4_t* o = reinterpret_cast<float4_t*>(a.partial + ((size_t)split * a.T + t) * dense_pitch(a.N) + n);
-      o[0] = lo;
-      o[1] = hi;
-      return;
-    }
-    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    end(a, t, v);
-  }
-  __device__ __forceinline__ void end(const DenseArgs& a, int t, float (&v)[8]) const {
-    const size_t r = (size_t)t * a.ldr + n;
-    float res[8] = {};
-    const bool whole = a.vector_io;  // N is a multiple of eight then
+  // Rows t, t + step, .. of those below T: v, eight values each, where eight columns of
+  // `out` and of the residual lie on 16-byte boundaries. The residual's loads come first.
+  __device__ __forceinline__ void finish(const DenseArgs& a, int t, int step, float (&v)[8 * kRows]) const {
+    u32x4_t lo[kRows], hi[kRows];
     if (a.residual) {
-      if (!whole) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) res[i] = i < count ? element(a.residual, r + i, a.residual_f32) : 0.f;
-      } else if (a.residual_f32) {
-        const float4_t* p = reinterpret_cast<const float4_t*>(static_cast<const float*>(a.residual) + r);
-        const float4_t lo = p[0], hi = p[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          res[i] = lo[i];
-          res[4 + i] = hi[i];
+      for (int r = 0; r < kRows; ++r) {
+        const size_t at = (size_t)min(t + r * step, a.T - 1) * a.ldr + n;
+        if (a.residual_f32) {
+          const u32x4_t* p = reinterpret_cast<const u32x4_t*>(static_cast<const float*>(a.residual) + at);
+          lo[r] = p[0];
+          hi[r] = p[1];
+        } else {
+          lo[r] = load16(a.residual, at);
         }
-      } else {
-        unpack8(load16(a.residual, r), res);
       }
     }
     if (a.bias)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += bias[i];
-    if (a.act != MOE_ACT_NONE)
+      for (int r = 0; r < kRows; ++r)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = activation(v[i], a.act);
-    if (a.residual)
+        for (int i = 0; i < 8; ++i) v[8 * r + i] += bias[i];
+    activate(a, v);
+    if (a.residual) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += res[i];
-    const size_t o = (size_t)t * a.N + n;
-    if (whole) {
+      for (int r = 0; r < kRows; ++r) {
+        float res[8];
+        if (a.residual_f32) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            res[i] = __uint_as_float(lo[r][i]);
+            res[4 + i] = __uint_as_float(hi[r][i]);
+          }
+        } else {
+          unpack8(lo[r], res);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * r + i] += res[i];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (t + r * step >= a.T) continue;
+      const size_t o = (size_t)(t + r * step) * a.N + n;
+      const float(&w)[8] = *reinterpret_cast<const float(*)[8]>(&v[8 * r]);
       if (a.out_f32) {
         float4_t* p = reinterpret_cast<float4_t*>(static_cast<float*>(a.out) + o);
-        p[0] = float4_t{v[0], v[1], v[2], v[3]};
-        p[1] = float4_t{v[4], v[5], v[6], v[7]};
+        p[0] = float4_t{w[0], w[1], w[2], w[3]};
+        p[1] = float4_t{w[4], w[5], w[6], w[7]};
       } else {
-        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.out) + o) = pack8(v);
+        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.out) + o) = pack8(w);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < count) {
-          if (a.out_f32)
-            static_cast<float*>(a.out)[o + i] = v[i];
-          else
-            static_cast<uint16_t*>(a.out)[o + i] = (uint16_t)bf16x2_bits(v[i], 0.f);
-        }
     }
   }
 };

@@ -193,67 +193,88 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& a, uint8_t* sm, int 
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     const int from = n0 + (wn * kNJ + t) * 16, below = t0 + (wm * kMJ + j0) * 16;
-    if (a.vector_io || a.splits > 1) {
-      const int c = lane % kLanes * 8;
-      const Columns cols(a, from + c);
-#pragma unroll 2
-      for (int r = lane / kLanes; r < 16 * S::kOutJ; r += kWave / kLanes) {
-        const float* v = mine + r * kPitch + c;
-        const float4_t lo = *reinterpret_cast<const float4_t*>(v), hi = *reinterpret_cast<const float4_t*>(v + 4);
-        if (below + r < a.T && from + c < a.N) cols.finish(a, below + r, split, lo, hi);
-      }
+    const int c = lane % kLanes * 8, r0 = lane / kLanes;
+    constexpr int kStep = kWave / kLanes, kRows = 16 * S::kOutJ, kAtOnce = kRows / kStep < 4 ? kRows / kStep : 4;
+    if (a.splits > 1) {
+      if (from + c < a.N)
+#pragma unroll 4
+        for (int r = r0; r < kRows && below + r < a.T; r += kStep) {
+          const float4_t* v = reinterpret_cast<const float4_t*>(mine + r * kPitch + c);
+          float4_t* o = reinterpret_cast<float4_t*>(a.partial + ((size_t)split * a.T + below + r) * dense_pitch(a.N) + from + c);
+          o[0] = v[0];
+          o[1] = v[1];
+        }
+    } else if (a.vector_io) {
+      const Columns<kAtOnce> cols(a, from + c);
+      if (from + c < a.N)
+#pragma unroll 1
+        for (int r = r0; r < kRows && below + r < a.T; r += kAtOnce * kStep) {
+          float v[8 * kAtOnce];
+#pragma unroll
+          for (int q = 0; q < kAtOnce; ++q)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float4_t u = *reinterpret_cast<const float4_t*>(mine + (r + q * kStep) * kPitch + c + 4 * i);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[8 * q + 4 * i + k] = u[k];
+            }
+          cols.finish(a, below + r, kStep, v);
+        }
     } else {  // rows that begin anywhere: neighbouring lanes store neighbouring columns
-      const int c = lane % kCols;
-      for (int r = lane / kCols; r < 16 * S::kOutJ; r += kWave / kCols)
-        if (below + r < a.T && from + c < a.N) finish(a, below + r, from + c, mine[r * kPitch + c]);
+      const int one = lane % kCols;
+      for (int r = lane / kCols; r < kRows; r += kWave / kCols)
+        if (below + r < a.T && from + one < a.N) finish(a, below + r, from + one, mine[r * kPitch + one]);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-// Workgroup `block` to tile: each XCD (workgroup id mod 8) takes a contiguous eighth of
-// them, in which kBand row tiles run beside each other, so that what neighbours share
-// meets in one L2; the parts of a tile's K are next to each other.
+// Tiles are numbered in bands of kBand row tiles, in a band column tile by column tile;
+// of `count` pieces of work from `first` on each XCD (workgroup id mod 8) takes a
+// contiguous eighth, so that what neighbours share meets in one L2.
 constexpr int kBand = 8;
-struct DenseTileAt {
-  int row, col, split;  // row < 0: none is left
+__device__ __forceinline__ int64_t dense_piece(int64_t count, int block) {
+  const int64_t share = (count + 7) / 8, i = (int64_t)(block & 7) * share + (block >> 3);
+  return (block >> 3) < share && i < count ? i : -1;
+}
+struct TilePlace {
+  int row, col;
 };
-__device__ __forceinline__ DenseTileAt dense_tile_at(int row_tiles, int col_tiles, int splits, int64_t all, int block) {
-  const int64_t share = (all + 7) / 8, i = (int64_t)(block & 7) * share + (block >> 3);
-  if ((block >> 3) >= share || i >= all) return DenseTileAt{-1, 0, 0};
-  const int64_t tile = i / splits, band = (int64_t)kBand * col_tiles;
+__device__ __forceinline__ TilePlace dense_place(int64_t tile, int row_tiles, int col_tiles) {
+  const int64_t band = (int64_t)kBand * col_tiles;
   const int first = (int)(tile / band) * kBand, rows = min(kBand, row_tiles - first), in = (int)(tile % band);
-  return DenseTileAt{first + in % rows, in / rows, (int)(i % splits)};
+  return TilePlace{first + in % rows, in / rows};
 }
 
+// The parts of a tile's K are next to each other.
 template <typename S>
 __global__ __launch_bounds__(S::kThreads, S::kWaves* S::kWgs / 4) void dense_tile_kernel(DenseArgs a, int row_tiles, int col_tiles) {
   __shared__ alignas(16) uint8_t sm[S::kLds];
-  const DenseTileAt at = dense_tile_at(row_tiles, col_tiles, a.splits, (int64_t)row_tiles * col_tiles * a.splits, blockIdx.x);
-  if (at.row >= 0) dense_tile<S>(a, sm, at.row * S::kM, at.col * S::kN, at.split);
+  const int64_t i = dense_piece((int64_t)row_tiles * col_tiles * a.splits, blockIdx.x);
+  if (i < 0) return;
+  const TilePlace at = dense_place(i / a.splits, row_tiles, col_tiles);
+  dense_tile<S>(a, sm, at.row * S::kM, at.col * S::kN, (int)(i % a.splits));
 }
 
 // The first `whole` tiles of S, the others as two halves of their rows, tiles of H.
 template <typename S, typename H>
-__global__ __launch_bounds__(S::kThreads, S::kWaves* S::kWgs / 4) void dense_tiles_kernel(DenseArgs a, int row_tiles, int col_tiles, int whole) {
+__global__ __launch_bounds__(S::kThreads, S::kWaves* S::kWgs / 4) void dense_halves_kernel(DenseArgs a, int row_tiles, int col_tiles, int whole) {
   static_assert(S::kM == 2 * H::kM && S::kN == H::kN && S::kThreads == H::kThreads, "halves");
   __shared__ alignas(16) uint8_t sm[S::kLds > H::kLds ? S::kLds : H::kLds];
   const int whole_blocks = (whole + 7) / 8 * 8;
   if ((int)blockIdx.x < whole_blocks) {
-    const DenseTileAt at = dense_tile_at(row_tiles, col_tiles, 1, whole, blockIdx.x);
-    if (at.row >= 0) dense_tile<S>(a, sm, at.row * S::kM, at.col * S::kN, 0);
-  } else {
-    const int rest = row_tiles * col_tiles - whole;
-    const int64_t share = (2 * (int64_t)rest + 7) / 8;
-    const int block = blockIdx.x - whole_blocks;
-    const int64_t i = (int64_t)(block & 7) * share + (block >> 3);
-    if ((block >> 3) >= share || i >= 2 * rest) return;
-    const int64_t tile = whole + i / 2, band = (int64_t)kBand * col_tiles;
-    const int first = (int)(tile / band) * kBand, rows = min(kBand, row_tiles - first), in = (int)(tile % band);
-    const int t0 = (first + in % rows) * S::kM + (int)(i & 1) * H::kM;
-    if (t0 < a.T) dense_tile<H>(a, sm, t0, in / rows * S::kN, 0);
+    const int64_t i = dense_piece(whole, blockIdx.x);
+    if (i < 0) return;
+    const TilePlace at = dense_place(i, row_tiles, col_tiles);
+    dense_tile<S>(a, sm, at.row * S::kM, at.col * S::kN, 0);
+    return;
   }
+  const int64_t i = dense_piece(2 * ((int64_t)row_tiles * col_tiles - whole), blockIdx.x - whole_blocks);
+  if (i < 0) return;
+  const TilePlace at = dense_place(whole + i / 2, row_tiles, col_tiles);
+  const int t0 = at.row * S::kM + (int)(i & 1) * H::kM;
+  if (t0 < a.T) dense_tile<H>(a, sm, t0, at.col * S::kN, 0);
 }
 
 // The parts of K, added in order: eight columns a thread.
@@ -262,9 +283,9 @@ __global__ __launch_bounds__(kJoinThreads) void dense_join_kernel(DenseArgs a, i
   const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
   const int t = (int)(i / groups);
   if (t >= a.T) return;
-  const Columns cols(a, (int)(i % groups) * 8);
+  const int n = (int)(i % groups) * 8;
   const size_t pitch = dense_pitch(a.N), step = (size_t)a.T * pitch;
-  const float* p = a.partial + (size_t)t * pitch + cols.n;
+  const float* p = a.partial + (size_t)t * pitch + n;
   float v[8] = {};
 #pragma unroll 4
   for (int s = 0; s < a.splits; ++s) {
@@ -275,7 +296,17 @@ __global__ __launch_bounds__(kJoinThreads) void dense_join_kernel(DenseArgs a, i
       v[4 + q] += hi[q];
     }
   }
-  cols.end(a, t, v);
+  if (a.vector_io) {
+    const Columns<1> cols(a, n);
+    cols.finish(a, t, 0, v);
+  } else {
+#pragma unroll 1
+    for (int q = 0; q < 8; ++q) {
+      if (n + q < a.N) finish(a, t, n + q, v[0]);
+#pragma unroll
+      for (int k = 0; k < 7; ++k) v[k] = v[k + 1];
+    }
+  }
 }
 
 template <typename S>
@@ -290,11 +321,11 @@ void launch(const DenseArgs& a, hipStream_t stream) {
 }
 
 template <typename S, typename H>
-void launch_both(const DenseArgs& a, hipStream_t stream) {
+void launch_halves(const DenseArgs& a, hipStream_t stream) {
   const int rows = (a.T + S::kM - 1) / S::kM, cols = (a.N + S::kN - 1) / S::kN;
-  const int64_t all = (int64_t)rows * cols, rest = all % 256;
-  const int64_t whole = all - rest;
-  hipLaunchKernelGGL((dense_tiles_kernel<S, H>), dim3((unsigned)((whole + 7) / 8 * 8 + (2 * rest + 7) / 8 * 8)), dim3(S::kThreads), 0, stream, a, rows, cols, (int)whole);
+  const int64_t all = (int64_t)rows * cols, rest = all % kCus, whole = all - rest;
+  hipLaunchKernelGGL((dense_halves_kernel<S, H>), dim3((unsigned)(whole + (2 * rest + 7) / 8 * 8)), dim3(S::kThreads), 0, stream, a, rows, cols,
+                     (int)whole);
 }
 
 }  // namespace
@@ -303,7 +334,7 @@ void launch_dense_tile(const DenseArgs& a, int shape, hipStream_t stream) {
   using Big = Shape<4, 8, 4, 2, 64, 2, 1>;
   switch (shape) {
     case kDenseHalves:
-      return launch_both<Big, Shape<4, 4, 2, 4, 64, 3, 1>>(a, stream);
+      return launch_halves<Big, Shape<4, 4, 2, 4, 64, 3, 1>>(a, stream);
     case kDense256x256:
       return launch<Big>(a, stream);
     case kDense128x128Two:
