@@ -29,6 +29,103 @@ constexpr int kScanParts = kRouteThreads / kScanExperts;
 constexpr int kFewChunks = 32;
 constexpr int kCountBatch = 16;  // counts that it requests at a time
 
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+
+// A bound that at least k of the wave's values reach, at most the k-th
+// largest: the largest such value found bit by bit below the leading bits that
+// all values share, ended as soon as exactly k reach it. Values of kNoKey and below
+// (no key, minus infinity) take no part; at least k others are needed.
+constexpr uint32_t kNoKey = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t kth_bound(uint32_t v, int k) {
+  const uint32_t hi = uniform(wave_max_u32(v)), d = hi ^ uniform(wave_min_u32(v > kNoKey ? v : 0xFFFFFFFFu));
+  if (d == 0) return hi;
+  int b = 31 - __builtin_clz(d), n_ge = -1;
+  uint32_t T = b == 31 ? 0u : (hi & ~((2u << b) - 1u));
+  for (; b >= 0 && n_ge != k; --b) {
+    const uint32_t c = T | (1u << b);
+    const int n = __popcll(__ballot(v >= c));
+    if (n >= k) {
+      T = c;
+      n_ge = n;
+    }
+  }
+  return T;
+}
+
+// One wave: the picks of a token by way of candidates. The exact keys (FP32 scores
+// rounded from FP64, plus the bias) are needed for the few experts only that can be
+// among the k largest. Approximate keys differ from the exact ones by at most 2^-22 +
+// 2^-23 |key|, both sides of which grow with the key, so an expert whose approximate
+// key is more than 2^-20 + 2^-21 |T| below a bound T that k of them reach has k
+// experts above it. The candidates, in expert order, one per lane, get their
+// exact keys and are ranked by them. Returns false, having written nothing,
+// where fewer than k lanes have finite keys or the candidates do not fit the wave (equal
+// scores of many experts): then every expert gets its exact key.
+// key: approximate, none NaN or infinity; in(j): whether expert lane + 64 j is
+// there and may be picked; exact(z): its score.
+template <int kPer, typename In, typename Exact>
+__device__ __forceinline__ bool pick_near(const float (&key)[kPer], const float (&z)[kPer], const float (&bias)[kPer], In in, int k, int lane,
+                                          Exact exact, int& id, float& s_mine, float& total) {
+  uint32_t top = 0u;  // 0: no expert (fewer than 64 of them, but k at least)
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) top = max(top, in(j) ? ordered_key(key[j]) : 0u);
+  if (__popcll(__ballot(top > kNoKey)) < k) return false;
+  const uint32_t t = kth_bound(top, k);
+  const float T = __uint_as_float((t & 0x80000000u) ? t ^ 0x80000000u : ~t);
+  const float low = T - (0x1p-20f + 0x1p-21f * fabsf(T));
+  uint64_t sel[kPer];
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    sel[j] = __ballot(in(j) && key[j] >= low);
+    n += __popcll(sel[j]);
+  }
+  if (n >= kWave) return false;  // lane 63 takes the pushes of lanes without a candidate
+
+  float cz = 0.f, cb = 0.f;
+  int ce = 0, base = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const uint64_t m = sel[j];
+    if (m != 0) {
+      const int cnt = __popcll(m);
+      const int below = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+      const int to = (((m >> lane) & 1ull) ? base + below : kWave - 1) * 4;
+      const float rz = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(z[j])));
+      const float rb = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(bias[j])));
+      const int re = __builtin_amdgcn_ds_permute(to, lane + kWave * j);
+      const bool here = lane >= base && lane < base + cnt;
+      cz = here ? rz : cz;
+      cb = here ? rb : cb;
+      ce = here ? re : ce;
+      base += cnt;
+    }
+  }
+  const float score = exact(cz);
+  const uint32_t mine = lane < n ? ordered_key(score + cb) : 0u;
+  int rank = 0;
+#pragma unroll 1  // unrolled, the compiler compares with all 64 lanes
+  for (int q0 = 0; q0 < n; q0 += 8) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {  // lanes past n: the key 0, below every candidate's
+      const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, q0 + q);
+      rank += other > mine || (other == mine && q0 + q < lane) ? 1 : 0;
+    }
+  }
+  const int to = (lane < n && rank < k ? rank : kWave - 1) * 4;
+  id = __builtin_amdgcn_ds_permute(to, ce);
+  s_mine = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(score)));
+  total = 0.f;
+  for (int r0 = 0; r0 < k; r0 += 8) {
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s_mine), r0 + q));
+#pragma unroll
+    for (int q = 0; q < 8; ++q) total = r0 + q < k ? total + v[q] : total;
+  }
+  return true;
+}
+
 // Tokens per workgroup when there are many: one or two per wave while that
 // gives the CUs two workgroups each (4,095 tokens x 896 experts: 25 us with 16,
 // 51 with 64), more (a mask's bits at most) where the counts of the chunks,

@@ -15,40 +15,12 @@
 namespace moe {
 namespace {
 
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
-
-// A bound that at least k of the wave's values reach, at most the k-th
-// largest: the largest such value found bit by bit below the leading bits that
-// all values share, ended as soon as exactly k reach it.
-__device__ __forceinline__ uint32_t kth_bound(uint32_t v, int k) {
-  const uint32_t hi = uniform(wave_max_u32(v)), d = hi ^ uniform(wave_min_u32(v));
-  if (d == 0) return hi;
-  int b = 31 - __builtin_clz(d), n_ge = -1;
-  uint32_t T = b == 31 ? 0u : (hi & ~((2u << b) - 1u));
-  for (; b >= 0 && n_ge != k; --b) {
-    const uint32_t c = T | (1u << b);
-    const int n = __popcll(__ballot(v >= c));
-    if (n >= k) {
-      T = c;
-      n_ge = n;
-    }
-  }
-  return T;
-}
-
-// One wave: the picks of a token by way of candidates. The exact keys (FP32
-// sigmoids rounded from FP64) are needed for the few experts only that can be
-// among the k largest. A key from the hardware's exp2 and reciprocal differs
-// from the exact one by at most
+// Approximate keys of a token's experts from the hardware's exp2 and reciprocal, which
+// differ from the exact ones by at most
 //   2^-22 (the sigmoid: its slope times the errors of the product with log2 e,
 //   the exponential and the reciprocal; |z| s (1 - s) < 0.23) + 2^-23 |key|
-//   (the roundings of the two additions of the bias),
-// both sides of which grow with the key, so an expert whose approximate key is
-// more than 2^-20 + 2^-21 |T| below a bound T that k of them reach has k
-// experts above it. The candidates, in expert order, one per lane, get their
-// exact keys and are ranked by them. Returns false, having written nothing,
-// where a key is NaN or infinity, fewer than k are finite, or the candidates do not fit the wave (equal
-// scores of many experts): then every expert gets its exact key.
+//   (the roundings of the two additions of the bias);
+// then the picks by way of candidates (rows_group.h).
 //
 // Measured (route_pick_kernel): 16,384 tokens x 256 experts, top-8, 22.7 us with
 // the exact key of every expert and 18.2 so; 4,095 x 896, top-16, BF16, 25.4
@@ -58,71 +30,16 @@ template <int kPer>
 __device__ __forceinline__ bool pick_candidates(const float (&z)[kPer], const float (&bias)[kPer], int E, int k, int lane,
                                                 int& id, float& s_mine, float& total) {
   float key[kPer];
-  uint32_t top = 0u;  // 0: no expert (fewer than 64 of them, but k at least)
   bool odd = false;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const float e = __builtin_amdgcn_exp2f(z[j] * -1.44269504088896341f);
     key[j] = __builtin_amdgcn_rcpf(1.f + e) + bias[j];
     odd |= !(key[j] < __builtin_inff());  // a bias of minus infinity: never among the k, see T
-    top = max(top, lane + kWave * j < E ? ordered_key(key[j]) : 0u);
   }
   if (__ballot(odd)) return false;
-  const uint32_t t = kth_bound(top, k);
-  const float T = __uint_as_float((t & 0x80000000u) ? t ^ 0x80000000u : ~t);
-  if (!(fabsf(T) < __builtin_inff())) return false;  // fewer than k finite keys
-  const float low = T - (0x1p-20f + 0x1p-21f * fabsf(T));
-  uint64_t sel[kPer];
-  int n = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    sel[j] = __ballot(lane + kWave * j < E && key[j] >= low);
-    n += __popcll(sel[j]);
-  }
-  if (n >= kWave) return false;  // lane 63 takes the pushes of lanes without a candidate
-
-  float cz = 0.f, cb = 0.f;
-  int ce = 0, base = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const uint64_t m = sel[j];
-    if (m != 0) {
-      const int cnt = __popcll(m);
-      const int below = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
-      const int to = (((m >> lane) & 1ull) ? base + below : kWave - 1) * 4;
-      const float rz = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(z[j])));
-      const float rb = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(bias[j])));
-      const int re = __builtin_amdgcn_ds_permute(to, lane + kWave * j);
-      const bool here = lane >= base && lane < base + cnt;
-      cz = here ? rz : cz;
-      cb = here ? rb : cb;
-      ce = here ? re : ce;
-      base += cnt;
-    }
-  }
-  const float score = sigmoid_f32(cz);
-  const uint32_t mine = lane < n ? ordered_key(score + cb) : 0u;
-  int rank = 0;
-#pragma unroll 1  // unrolled, the compiler compares with all 64 lanes
-  for (int q0 = 0; q0 < n; q0 += 8) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {  // lanes past n: the key 0, below every candidate's
-      const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, q0 + q);
-      rank += other > mine || (other == mine && q0 + q < lane) ? 1 : 0;
-    }
-  }
-  const int to = (lane < n && rank < k ? rank : kWave - 1) * 4;
-  id = __builtin_amdgcn_ds_permute(to, ce);
-  s_mine = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(score)));
-  total = 0.f;
-  for (int r0 = 0; r0 < k; r0 += 8) {
-    float v[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s_mine), r0 + q));
-#pragma unroll
-    for (int q = 0; q < 8; ++q) total = r0 + q < k ? total + v[q] : total;
-  }
-  return true;
+  const auto any = [&](int j) { return lane + kWave * j < E; };
+  return pick_near<kPer>(key, z, bias, any, k, lane, [](float v) { return sigmoid_f32(v); }, id, s_mine, total);
 }
 
 // The workgroup's chunk of n tokens from t0 on, a token per wave at a time (the

@@ -2,11 +2,13 @@
 // sigmoid or softmax scores, limited to the best groups of experts, and the routes
 // grouped by expert.
 //
-// One wave per token: lane l holds experts l + 64 j. Every expert's score comes from
-// FP64 and every key is exact, so the picks are those of the definition; the groups'
-// two largest keys are found through LDS, where a group's experts lie side by side;
-// the picks are route_device.h's, with keys of 0 (below every expert's) where the
-// group takes no part. The grouping of the routes is rows_group.h's.
+// One wave per token: lane l holds experts l + 64 j. The picks are those of the exact
+// keys, FP32 roundings of FP64 scores. Softmax scores are exact for all experts, since
+// the sum needs every exponential in FP64 anyway; sigmoid scores are the hardware's
+// first, which choose groups (where the least of the chosen and the best of the others
+// lie further apart than their errors) and candidates, and only the candidates get
+// exact ones. The groups' largest keys are found through LDS, where a group's experts
+// lie side by side. The grouping of the routes is rows_group.h's.
 #include <hip/hip_runtime.h>
 
 #include "../../include/moe_block.h"
@@ -16,113 +18,206 @@
 namespace moe {
 namespace {
 
-// FP32 scores of a token's logits, rounded from FP64.
-template <int kPer>
-__device__ __forceinline__ void scores_of(const float (&z)[kPer], bool softmax, int E, int lane, float (&s)[kPer]) {
-  if (!softmax) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) s[j] = sigmoid_f32(z[j]);
-    return;
-  }
-  uint32_t top = 0u;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) top = max(top, lane + kWave * j < E ? ordered_key(z[j]) : 0u);
-  top = wave_max_u32(top);
-  const float m = __uint_as_float((top & 0x80000000u) ? top ^ 0x80000000u : ~top);
-  const double from = m == -__builtin_inff() ? 0.0 : (double)m;
-  double e[kPer], sum = 0.0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    e[j] = lane + kWave * j < E ? exp((double)z[j] - from) : 0.0;
-    sum += e[j];
-  }
-  sum = wave_sum_f64(sum);
-  const double inv = sum == 0.0 ? 0.0 : 1.0 / sum;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) s[j] = (float)(e[j] * inv);
+// exp(x) for x <= 0 within 2^-47 of its value: 2^(n / 32) by table, where n is the
+// nearest integer to 32 x / ln 2, and five terms for what is left (at most ln 2 / 64;
+// the sixth term is 2^-48.7). The 32 values of the table are the LDS's 64 banks, so
+// lanes that differ in entry differ in bank. Twelve FP64 instructions, where the
+// library's exponential has twice as many.
+constexpr int kExpParts = 32;
+__device__ __forceinline__ double exp_below_0(double x, const double* table) {
+  x = fmax(x, -800.0);  // 0 as FP32, and far below any sum's last bit
+  const double n = rint(x * (kExpParts * 1.4426950408889634));
+  double r = fma(n, -0x1.62e42fee00000p-6, x);  // ln 2 / 32 in two parts
+  r = fma(n, -0x1.a39ef35793c76p-38, r);
+  const double p = fma(r, fma(r, fma(r, fma(r, fma(r, 1.0 / 120.0, 1.0 / 24.0), 1.0 / 6.0), 0.5), 1.0), 1.0);
+  const int i = (int)n;
+  return ldexp(table[i & (kExpParts - 1)] * p, i >> 5);
 }
 
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
 
-// Clears the keys of experts outside the top_groups groups. at[j]: the first lane of
-// the group of expert lane + 64 j (a group has `lanes` lanes, a power of two).
-// `keys`: LDS of the wave's own.
+// The softmax of a token's logits, FP32 roundings of FP64 values.
 template <int kPer>
-__device__ __forceinline__ void limit_groups(const moe_route_scored_args& a, int lanes, const int (&at)[kPer], uint32_t* keys, int lane,
-                                             uint32_t (&kv)[kPer]) {
-  const int G = a.groups, size = a.route.E / G, g = lane / lanes;
+__device__ __forceinline__ void softmax_of(const float (&z)[kPer], int E, int lane, const double* table, float (&s)[kPer]) {
+  uint32_t top = 0u;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) keys[lane + kWave * j] = kv[j];
+  for (int j = 0; j < kPer; ++j) top = max(top, lane + kWave * j < E ? ordered_key(z[j]) : 0u);
+  const float m = key_value(wave_max_u32(top));
+  const double from = m == -__builtin_inff() ? 0.0 : (double)m;
+  double e[kPer], sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    e[j] = lane + kWave * j < E ? exp_below_0((double)z[j] - from, table) : 0.0;
+    sum += e[j];
+    if (j % 2) __builtin_amdgcn_sched_barrier(0);  // all at once, they would take the registers of the logits
+  }
+  sum = wave_sum_f64(sum);
+  // of minus infinities alone the sum is E times the exponential of -800: their scores are 0
+  const double inv = m == -__builtin_inff() ? 0.0 : 1.0 / sum;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) s[j] = (float)(e[j] * inv);
+}
+
+// A group's two largest keys (b1 >= b2) with those of other lanes.
+__device__ __forceinline__ void merge(float& b1, float& b2, float c1, float c2) {
+  b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
+  b1 = fmaxf(b1, c1);
+}
+template <int kControl>
+__device__ __forceinline__ void merge_dpp(float& b1, float& b2) {  // by a permutation inside rows of 16
+  const int c1 = __builtin_amdgcn_mov_dpp(__float_as_int(b1), kControl, 0xF, 0xF, false);
+  const int c2 = __builtin_amdgcn_mov_dpp(__float_as_int(b2), kControl, 0xF, 0xF, false);
+  merge(b1, b2, __int_as_float(c1), __int_as_float(c2));
+}
+
+// The groups that take part, as a mask of their first lanes (a group has `lanes` lanes,
+// a power of two), by the keys. `near`: the keys are up to 2^-22 + 2^-23 |key| off;
+// false where that leaves it open whether some group takes part. Without, equal groups
+// go by their index. `keys`: LDS of the wave's own, 16-byte aligned.
+template <int kPer>
+__device__ __forceinline__ bool best_groups(const moe_route_scored_args& a, int lanes, const float (&key)[kPer], bool near, float* keys, int lane,
+                                            uint64_t& in) {
+  // opaque, so that nothing that follows from these is kept for the next token: where it was, it went
+  // to scratch memory (16,384 tokens x 256 experts in 8 groups, 25.0 us with it and 21 without)
+  int G = a.groups, size = a.route.E / a.groups;
+  asm volatile("" : "+s"(G), "+s"(size), "+s"(lanes), "+v"(lane));
+  const int g = lane >> (31 - __builtin_clz(lanes)), sub = lane & (lanes - 1);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) keys[lane + kWave * j] = key[j];
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
-  uint32_t b1 = 0u, b2 = 0u;  // the group's largest keys
-  if (g < G)
-    for (int i = lane & (lanes - 1); i < size; i += lanes) {
-      const uint32_t v = keys[g * size + i];
-      b2 = max(b2, min(b1, v));
-      b1 = max(b1, v);
+  float b1 = -__builtin_inff(), b2 = b1;  // the group's largest keys
+  const float* const of_group = keys + min(g, G - 1) * size;
+  if (size % (4 * lanes) == 0) {
+#pragma unroll 1
+    for (int i = 4 * sub; i < size; i += 4 * lanes) {
+      const float4_t v = *reinterpret_cast<const float4_t*>(of_group + i);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        b2 = __builtin_amdgcn_fmed3f(b1, b2, v[q]);
+        b1 = fmaxf(b1, v[q]);
+      }
     }
+  } else {
+#pragma unroll 1
+    for (int i = sub; i < size; i += 4 * lanes) {
+      float v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = of_group[min(i + q * lanes, size - 1)];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float u = i + q * lanes < size ? v[q] : -__builtin_inff();
+        b2 = __builtin_amdgcn_fmed3f(b1, b2, u);
+        b1 = fmaxf(b1, u);
+      }
+    }
+  }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
-  for (int o = 1; o < lanes; o <<= 1) {
-    const uint32_t c1 = __shfl_xor(b1, o, kWave), c2 = __shfl_xor(b2, o, kWave);
-    b2 = max(max(b2, c2), min(b1, c1));
-    b1 = max(b1, c1);
+  if (lanes > 1) merge_dpp<0xB1>(b1, b2);   // swap neighbours
+  if (lanes > 2) merge_dpp<0x4E>(b1, b2);   // swap pairs
+  if (lanes > 4) merge_dpp<0x141>(b1, b2);  // half-row mirror
+  if (lanes > 8) merge_dpp<0x140>(b1, b2);  // row mirror
+#pragma unroll 1
+  for (int o = 16; o < lanes; o <<= 1) merge(b1, b2, __shfl_xor(b1, o, kWave), __shfl_xor(b2, o, kWave));
+  const float value = a.group_best == 2 ? b1 + b2 : b1;
+  // groups surely ahead of the lane's own, and those that may be (itself among the latter)
+  const float off = near ? 0x1p-18f + 0x1p-19f * fabsf(value) : 0.f, over = value + off, under = value - off;
+  const auto ahead = [&](float other, int q) { return other > over || (!near && other == value && q < g); };
+  const auto maybe = [&](float other, int q) { return near ? other > under : ahead(other, q) || q == g; };
+  int sure = 0, may = 0;
+  if (G <= lanes) {  // a group's lanes compare it with one other each
+    const float other = __shfl(value, sub * lanes, kWave);
+    const bool there = sub < G;
+    const uint64_t s = __ballot(there && ahead(other, sub)), m = __ballot(there && maybe(other, sub));
+    const uint64_t field = lanes == kWave ? ~0ull : (1ull << lanes) - 1ull;
+    const int first = lane & ~(lanes - 1);
+    sure = __popcll((s >> first) & field);
+    may = __popcll((m >> first) & field);
+  } else {
+#pragma unroll 2
+    for (int q = 0; q < G; ++q) {
+      const float other = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), q * lanes));
+      sure += ahead(other, q) ? 1 : 0;
+      may += maybe(other, q) ? 1 : 0;
+    }
   }
-  const uint32_t mine = ordered_key(a.group_best == 2 ? key_value(b1) + key_value(b2) : key_value(b1));
-  int rank = 0;
-  for (int q = 0; q < G; ++q) {
-    const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, q * lanes);
-    rank += other > mine || (other == mine && q < g) ? 1 : 0;
-  }
-  const uint64_t in = __ballot(g < G && rank < a.top_groups);
+  in = __ballot(g < G && may <= a.top_groups);
+  return __ballot(g < G && may > a.top_groups && sure < a.top_groups) == 0;
+}
+
+struct Pick {
+  int id;
+  float s, total;
+};
+
+// The picks of token t by the exact keys of all experts: for keys that are NaN or
+// infinite, groups or candidates too close to tell apart.
+template <int kPer, bool kGroups, bool kSoftmax>
+__device__ __forceinline__ Pick pick_exactly(const moe_route_scored_args& sa, int t, int lanes, float* keys, const double* table) {
+  const moe_route_args& a = sa.route;
+  const int lane = threadIdx.x & (kWave - 1);
+  const bool bf16 = a.logits_dtype == MOE_DTYPE_BF16;
+  const size_t row = (size_t)t * a.E;
+  int at[kPer];
+  float z[kPer], score[kPer], key[kPer];
+  uint32_t kv[kPer];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) kv[j] = (in >> at[j]) & 1ull ? kv[j] : 0u;
+  for (int j = 0; j < kPer; ++j) at[j] = min(lane + kWave * j, a.E - 1);
+  load_logits<kPer>(bf16 ? (const void*)((const uint16_t*)a.logits + row) : (const void*)((const uint32_t*)a.logits + row), bf16, at, z);
+  if (kSoftmax) softmax_of<kPer>(z, a.E, lane, table, score);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (!kSoftmax) score[j] = sigmoid_f32(z[j]);
+    key[j] = a.bias ? score[j] + a.bias[at[j]] : score[j];
+    kv[j] = lane + kWave * j < a.E ? max(ordered_key(key[j]), 1u) : 0u;  // a NaN with every bit set would be 0
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (kGroups) {
+    uint64_t in;
+    best_groups<kPer>(sa, lanes, key, false, keys, lane, in);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) kv[j] = (in >> (at[j] / (a.E / sa.groups) * lanes)) & 1ull ? kv[j] : 0u;
+  }
+  Pick p;
+  pick_top_k<kPer>(kv, score, a.E, a.k, lane, p.id, p.s, p.total);
+  return p;
 }
 
 // As rows_route.hip's route_chunk, by scores and groups. `keys`: LDS, kPer * 64
-// values a wave, where there are groups.
-template <int kPer, bool kGroups>
+// values a wave, where there are groups; `table`: LDS.
+template <int kPer, bool kGroups, bool kSoftmax>
 __device__ __forceinline__ void scored_chunk(const moe_route_scored_args& sa, int t0, int n, int* picks, unsigned long long* mask,
-                                             uint32_t* keys) {
+                                             float* keys, double* table) {
   const moe_route_args& a = sa.route;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const bool bf16 = a.logits_dtype == MOE_DTYPE_BF16;
-  int at[kPer], group[kPer];
+  constexpr bool kAhead = kPer < 16;  // the next token's logits on their way: 16 a lane leave no registers for it
+  const auto expert = [&](int j) { return min(lane + kWave * j, a.E - 1); };
   float bias[kPer], next[kPer];
   const auto request = [&](int i) {
     const size_t row = (size_t)(t0 + i) * a.E;
+    int at[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) at[j] = expert(j);
     load_logits<kPer>(bf16 ? (const void*)((const uint16_t*)a.logits + row) : (const void*)((const uint32_t*)a.logits + row),
                       bf16, at, next);
   };
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) at[j] = min(lane + kWave * j, a.E - 1);
-  int i = wave;
+  int i = __builtin_amdgcn_readfirstlane(wave);
   if (i < n) request(i);
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) bias[j] = a.bias ? a.bias[at[j]] : 0.f;
+  for (int j = 0; j < kPer; ++j) bias[j] = a.bias ? a.bias[expert(j)] : 0.f;
   int lanes = kWave;
+  uint32_t group[(kPer + 3) / 4] = {};  // the first lanes of the experts' groups, a byte each
   if (kGroups) {
     while (lanes * sa.groups > kWave) lanes >>= 1;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) group[j] = at[j] / (a.E / sa.groups) * lanes;
+    for (int j = 0; j < kPer; ++j) group[j / 4] |= (uint32_t)(expert(j) / (a.E / sa.groups) * lanes) << (8 * (j % 4));
   }
   for (int e = threadIdx.x; e < a.local_experts; e += kRouteThreads) mask[e] = 0ull;
+  if (threadIdx.x < kExpParts) table[threadIdx.x] = exp2((double)threadIdx.x / kExpParts);
   __syncthreads();
-  for (; i < n; i += kRouteWaves) {
-    float z[kPer], score[kPer];
-    uint32_t key[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) z[j] = next[j];
-    if (i + kRouteWaves < n) request(i + kRouteWaves);
-    scores_of<kPer>(z, sa.scores == MOE_SCORES_SOFTMAX, a.E, lane, score);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)  // a NaN with every bit set would have the key 0
-      key[j] = lane + kWave * j < a.E ? max(ordered_key(a.bias ? score[j] + bias[j] : score[j]), 1u) : 0u;
-    if (kGroups) limit_groups<kPer>(sa, lanes, group, keys + wave * kPer * kWave, lane, key);
-    int id;
-    float s, total;
-    pick_top_k<kPer>(key, score, a.E, a.k, lane, id, s, total);
+  const auto write = [&](int i, int id, float s, float total) {
     if (lane < a.k) {
       const size_t r = (size_t)(t0 + i) * a.k + lane;
       a.ids[r] = id;
@@ -132,33 +227,88 @@ __device__ __forceinline__ void scored_chunk(const moe_route_scored_args& sa, in
       if (local) atomicOr(&mask[e], 1ull << i);
       if (picks) picks[i * a.k + lane] = local ? e : -1;
     }
+  };
+  uint64_t left = 0;  // tokens of this wave that the candidates do not settle
+  for (; i < n; i += kRouteWaves) {
+    float z[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) z[j] = next[j];
+    if (kAhead && i + kRouteWaves < n) request(i + kRouteWaves);
+    int id;
+    float s, total;
+    uint64_t in_groups = ~0ull;
+    const auto takes_part = [&](int j) { return ((in_groups >> (group[j / 4] >> (8 * (j % 4)) & 0xFFu)) & 1ull) != 0; };
+    const auto in = [&](int j) { return lane + kWave * j < a.E; };
+    const auto leave_out = [&](float (&key)[kPer]) {  // minus infinity: never among the candidates
+#pragma unroll
+      for (int j = 0; j < (kPer + 3) / 4; ++j) asm volatile("" : "+v"(group[j]));  // as in best_groups
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) key[j] = takes_part(j) ? key[j] : -__builtin_inff();
+    };
+    float key[kPer];
+    bool done = false, odd = false;
+    if (kSoftmax) softmax_of<kPer>(z, a.E, lane, table, z);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      key[j] = (kSoftmax ? z[j] : __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z[j] * -1.44269504088896341f))) + bias[j];
+      odd |= !(key[j] < __builtin_inff());
+    }
+    if (__ballot(odd) == 0) {
+      bool sure = true;
+      if (kGroups) {
+        sure = best_groups<kPer>(sa, lanes, key, !kSoftmax, keys + wave * kPer * kWave, lane, in_groups);
+        leave_out(key);
+      }
+      const auto exact = [](float v) { return kSoftmax ? v : sigmoid_f32(v); };
+      if (sure) done = pick_near<kPer>(key, z, bias, in, a.k, lane, exact, id, s, total);
+    }
+    if (done)
+      write(i, id, s, total);
+    else
+      left |= 1ull << i;
+    if (!kAhead && i + kRouteWaves < n) request(i + kRouteWaves);
+  }
+  for (; left != 0; left &= left - 1) {  // apart, so that it takes no registers from the usual way
+    const int at = __builtin_ctzll(left);
+    const Pick p = pick_exactly<kPer, kGroups, kSoftmax>(sa, t0 + at, lanes, keys + wave * kPer * kWave, table);
+    write(at, p.id, p.s, p.total);
   }
   __syncthreads();
 }
 
-template <int kPer, bool kGroups>
+template <int kPer, bool kGroups, bool kSoftmax>
 __global__ __launch_bounds__(kRouteThreads) void scored_one_kernel(moe_route_scored_args a) {
   __shared__ RouteShared sm;
-  __shared__ uint32_t keys[kGroups ? kRouteWaves * kPer * kWave : 1];
-  scored_chunk<kPer, kGroups>(a, 0, a.route.T, sm.picks, sm.mask, keys);
+  __shared__ alignas(16) float keys[kGroups ? kRouteWaves * kPer * kWave : 1];
+  __shared__ double table[kExpParts];
+  scored_chunk<kPer, kGroups, kSoftmax>(a, 0, a.route.T, sm.picks, sm.mask, keys, table);
   group_one(a.route, sm);
 }
 
-template <int kPer, bool kGroups>
-__global__ __launch_bounds__(kRouteThreads) void scored_pick_kernel(moe_route_scored_args a) {
+template <int kPer, bool kGroups, bool kSoftmax>
+__global__ __launch_bounds__(kRouteThreads, kPer <= 4 ? 8 : 4) void scored_pick_kernel(moe_route_scored_args a) {
   __shared__ unsigned long long mask[MOE_DECODE_MAX_EXPERTS];
-  __shared__ uint32_t keys[kGroups ? kRouteWaves * kPer * kWave : 1];
+  __shared__ alignas(16) float keys[kGroups ? kRouteWaves * kPer * kWave : 1];
+  __shared__ double table[kExpParts];
   const int chunk = chunk_tokens(a.route.T), t0 = blockIdx.x * chunk, n = min(chunk, a.route.T - t0);
-  scored_chunk<kPer, kGroups>(a, t0, n, nullptr, mask, keys);
+  scored_chunk<kPer, kGroups, kSoftmax>(a, t0, n, nullptr, mask, keys, table);
   write_counts(a.route, mask);
+}
+
+template <int kPer, bool kGroups>
+void launch_scored(const moe_route_scored_args& a, hipStream_t stream) {
+  if (a.scores == MOE_SCORES_SOFTMAX)
+    launch_grouping(a.route, scored_one_kernel<kPer, kGroups, true>, scored_pick_kernel<kPer, kGroups, true>, a, stream);
+  else
+    launch_grouping(a.route, scored_one_kernel<kPer, kGroups, false>, scored_pick_kernel<kPer, kGroups, false>, a, stream);
 }
 
 template <int kPer>
 void launch_scored(const moe_route_scored_args& a, hipStream_t stream) {
   if (a.top_groups < a.groups)  // else every group takes part
-    launch_grouping(a.route, scored_one_kernel<kPer, true>, scored_pick_kernel<kPer, true>, a, stream);
+    launch_scored<kPer, true>(a, stream);
   else
-    launch_grouping(a.route, scored_one_kernel<kPer, false>, scored_pick_kernel<kPer, false>, a, stream);
+    launch_scored<kPer, false>(a, stream);
 }
 
 }  // namespace
