@@ -5,9 +5,10 @@
 // As rows_norm.hip: one workgroup per token holds the whole row in registers, eight
 // columns a lane and chunk, so every input is read once and every output written once.
 // The second norm's statistics need the first's, so a row crosses the workgroup
-// twice; both sums of squares are taken in FP64, and the normalised and gated row
-// stays in FP64 up to its sum with the residual: three roundings less on the way to
-// the 8-bit codes than with FP32 products, for two FP64 products a value.
+// twice. Both sums of squares are taken in FP64, the way from a block's output to the
+// residual's row in FP32 with four roundings (in FP64, without three of them, it cost
+// 8,191 x 3584 72 us instead of 68: the vector instructions show). Bound by HBM: these
+// at 4.8 TB/s, 4,096 tokens of eight rows of 7168 at 4.6; a large copy runs at 5.2.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -50,10 +51,9 @@ __global__ __launch_bounds__(kChunks == 4 ? 512 : 1024) void join_kernel(moe_joi
     u[c] = ja.gate_kind >= MOE_GATE_COLUMN ? load16(ja.gate, ja.gate_kind == MOE_GATE_FULL ? row + at : (size_t)at) : zero;
     g[c] = a.gamma ? load16(a.gamma, at) : zero;
   }
-  double gate = 1.0;  // of the token
+  float gate = 1.f;  // of the token
   if (ja.gate_kind == MOE_GATE_ROW)
-    gate = (double)(ja.gate_dtype == MOE_DTYPE_BF16 ? bf16_value(static_cast<const uint16_t*>(ja.gate)[t])
-                                                    : static_cast<const float*>(ja.gate)[t]);
+    gate = ja.gate_dtype == MOE_DTYPE_BF16 ? bf16_value(static_cast<const uint16_t*>(ja.gate)[t]) : static_cast<const float*>(ja.gate)[t];
 
   double sq = 0.0;
 #pragma unroll
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(kChunks == 4 ? 512 : 1024) void join_kernel(moe_joi
       sq = fma((double)h[c][i], (double)h[c][i], sq);
     }
   }
-  const double rstd_post = ja.post_gamma ? row_rstd(sq, part[0], a.D, ja.post_eps) : 1.0;
+  const float rstd_post = ja.post_gamma ? (float)row_rstd(sq, part[0], a.D, ja.post_eps) : 1.f;
   sq = 0.0;
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
@@ -110,9 +110,9 @@ __global__ __launch_bounds__(kChunks == 4 ? 512 : 1024) void join_kernel(moe_joi
     unpack8(p[c], pv);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      double by = ja.gate_kind >= MOE_GATE_COLUMN ? (double)uv[i] : gate;
-      if (ja.post_gamma) by *= rstd_post * (double)(pv[i] + ja.gamma_offset);
-      const float v = (float)fma((double)h[c][i], by, (double)rv[i] * (double)ja.residual_scale);
+      float by = ja.gate_kind >= MOE_GATE_COLUMN ? uv[i] : gate;
+      if (ja.post_gamma) by *= rstd_post * (pv[i] + ja.gamma_offset);
+      const float v = fmaf(h[c][i], by, rv[i] * ja.residual_scale);
       h[c][i] = live ? v : 0.f;
       sq = fma((double)h[c][i], (double)h[c][i], sq);
     }
@@ -166,10 +166,16 @@ extern "C" int moe_join_rmsnorm_quant(const moe_join_args* args, void* stream) {
   const int lanes = a.norm.D / kVec;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const auto waves = [](int n) { return (n + kWave - 1) / kWave * kWave; };
-  const bool wide = a.norm.k > 0 || a.norm.T <= kFewTokens;
-  if (lanes <= (wide ? 1024 : 256))
+  // Chunks a lane. Few plain tokens: one, with all of a row's loads on their way at once.
+  // Routed rows of more than 2048 columns: two, so that a CU holds two workgroups, of which
+  // one loads while the other is between its barriers (4,096 tokens of eight rows of 7168:
+  // 178 us with one chunk, 158 with two, 164 with four; 3584: 81, 79 and 89). Many plain
+  // rows: two up to 4096 columns, four beyond (8,191 x 3584: 73, 68 and 71 us; 4,096 x 8192:
+  // 73, 66 and 64).
+  const bool few = a.norm.k == 0 && a.norm.T <= kFewTokens;
+  if (lanes <= (few ? 1024 : 256))
     launch_join<1>(a, waves(lanes), s);
-  else if (wide || lanes <= 512)
+  else if (few || a.norm.k > 0 || lanes <= 512)
     launch_join<2>(a, waves((lanes + 1) / 2), s);
   else
     launch_join<4>(a, waves((lanes + 3) / 4), s);

@@ -135,12 +135,12 @@ int moe_route_rows_scored(const moe_route_scored_args* a, void* stream);
  *   b = delta[t] + sum_j weights[t, j] * y[pos[t, j]]
  *       summed in FP64 in this order and rounded to FP32 (a position outside
  *       [0, R) adds nothing);
- *   n = b * rstd(b) * (post_gamma + gamma_offset), or b without post_gamma,
- *       rstd(b) = 1 / sqrt(sum_i b_i^2 / D + post_eps), in FP64 but for the FP32
- *       addition of gamma_offset;
- *   h = residual_scale * residual[t] + gate * n, in FP64, rounded to FP32 once;
- *   v = (h * FP32(rstd(h))) * (gamma + gamma_offset) in FP32, or h without gamma,
- *       with eps, the statistics in FP64;
+ *   c = rstd(b) * (post_gamma + gamma_offset), or 1 without post_gamma,
+ *       rstd(b) = FP32(1 / sqrt(sum_i b_i^2 / D + post_eps)), the statistics in FP64;
+ *   h = b * (gate * c) + residual_scale * residual[t], where gate * c and the
+ *       products in it are FP32, the residual's too, and the sum with b's product is
+ *       rounded once;
+ *   v = (h * rstd(h)) * (gamma + gamma_offset) in FP32, with eps, or h without gamma;
  *   residual_out[t] = BF16(h), out[t] = BF16(v), q[t] and scale[t] = the 8-bit
  *   form of v (not of BF16(v)).
  * T and k choose the order of the statistics' sums, which may move the last bit of

@@ -88,19 +88,23 @@ def route_scored(logits, bias, top_k: int, routed_scale: float, *, kind: str = "
 
 
 def _rstd(h, eps):
-    return 1.0 / np.sqrt((h * h).mean(axis=1, keepdims=True) + float(f32(eps)))
+    return f32(1.0 / np.sqrt((h * h).mean(axis=1, keepdims=True) + float(f32(eps))))
 
 
 def join_rows(residual, delta, y, pos, weights, *, gamma, eps, post_gamma=None, post_eps=None, gate=None, residual_scale=1.0,
               gamma_offset=0.0):
-    """(h, v): the residual row, float64 up to its one rounding, and its
-    normalised form, binary32 values; gate broadcasts against [T, D]."""
+    """(h, v): the residual row and its normalised form, binary32 values; gate
+    broadcasts against [T, D]. Products and the additions of gamma_offset are
+    rounded to binary32, b's product with its factor only with the sum."""
     b = np.asarray(sum_rows(None, delta, y, pos, weights), np.float64)
-    plus = lambda g: np.asarray(f32(np.asarray(g, np.float64) + float(f32(gamma_offset))), np.float64)  # noqa: E731
+    plus = lambda g: f32(np.asarray(g, np.float64) + float(f32(gamma_offset)))  # noqa: E731
+    factor = np.float64(1.0)
     if post_gamma is not None:
-        b = b * _rstd(b, eps if post_eps is None else post_eps) * plus(post_gamma)
-    h = b * (1.0 if gate is None else np.asarray(gate, np.float64))
+        factor = f32(_rstd(b, eps if post_eps is None else post_eps) * plus(post_gamma))
+    if gate is not None:
+        factor = f32(factor * np.asarray(gate, np.float64))
+    h = b * factor
     if residual is not None:
-        h = h + np.asarray(residual, np.float64) * float(f32(residual_scale))
+        h = h + f32(np.asarray(residual, np.float64) * float(f32(residual_scale)))
     h = np.asarray(f32(h), np.float64)
-    return h, h if gamma is None else f32(f32(h * f32(_rstd(h, eps))) * plus(gamma))
+    return h, h if gamma is None else f32(f32(h * _rstd(h, eps)) * plus(gamma))

@@ -1,13 +1,13 @@
 """moe_join_rmsnorm_quant on the GPU against oracle/block.py.
 
-The sums, the statistics and the way to the residual row are FP64 on both sides
-and every other step is one binary32 operation, so residual, rows, codes and
-scales have to be bit-equal, but for values next to a rounding border: the
-second rstd (FP64 sums of at most 16,384 terms in different orders differ by
-less than 2^-38 of their magnitude: one row in 2^13 at most), an element of the
-residual row (the same of the first rstd: one in 2^13 if the sums' orders did
-their worst, some 2^-50 and one in 2^25 as they come) and a sum of weighted rows
-(within 2^-47, one in 2^22). The inputs are seeded, so a pass stays a pass."""
+The sums and the statistics are FP64 on both sides and every other step is one
+binary32 operation, so residual, rows, codes and scales have to be bit-equal,
+but for values next to a rounding border: an rstd (FP64 sums of at most 16,384
+terms in different orders differ by less than 2^-38 of their magnitude: one row
+in 2^13 at most), a sum of weighted rows (the order of its terms is the same on
+both sides but NumPy's: within 2^-47, one in 2^22) and the sum that gives the
+residual's row (rounded once on the GPU, by way of float64 in NumPy: one in
+2^28). The inputs are seeded, so a pass stays a pass."""
 
 from __future__ import annotations
 
