@@ -10,6 +10,7 @@ synchronise, so they can be captured into a graph.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional
 
@@ -50,6 +51,10 @@ class JoinArgs(ctypes.Structure):
 def _matrix(t, name, dtypes, dev, shape, unit):
     """(address, row stride) of a matrix whose rows are contiguous, `unit`
     values between row starts and 2 * unit (BF16) bytes their alignment."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.device == dev and t.is_contiguous():
+        p = t.data_ptr()  # the usual case, without what the others are told
+        if p % 16 == 0:
+            return p, shape[1]
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
     if t.shape != shape:
@@ -73,6 +78,11 @@ def _matrix(t, name, dtypes, dev, shape, unit):
     return p, ld if rows > 1 else columns
 
 
+@functools.lru_cache(maxsize=4096)
+def _dense_workspace(T, N, K) -> int:
+    return lib().moe_dense_gemm_workspace(T, N, K)
+
+
 def dense_gemm(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = None, act: Optional[str] = None,
                residual: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """[T, N] = act(x w^T + bias) + residual (include/moe_block.h).
@@ -89,7 +99,8 @@ def dense_gemm(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor]
         raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("x must be a [T, K] and w an [N, K] tensor")
-    (T, K), N, dev = x.shape, w.shape[0], x.device
+    T, K = x.shape
+    N, dev = w.shape[0], x.device
     if T > ROWS_MAX_TOKENS:
         raise ValueError(f"at most {ROWS_MAX_TOKENS} rows, got {T}")
     if K % 8 or not 8 <= K <= DENSE_MAX_DIM or not 1 <= N <= DENSE_MAX_DIM:
@@ -108,7 +119,7 @@ def dense_gemm(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor]
     with _where(dev, stream, x, w, bias, residual):
         out = torch.empty((T, N), dtype=out_dtype, device=dev)
         if T:
-            need = lib().moe_dense_gemm_workspace(T, N, K)
+            need = _dense_workspace(T, N, K)
             ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
             _call("moe_dense_gemm",
                   DenseArgs(T, N, K, ACTS[act], _DTYPES[out_dtype], bias_dtype, residual_dtype, ldx, ldw, ldr, xp, wp, bp, rp,

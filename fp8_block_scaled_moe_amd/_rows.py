@@ -112,11 +112,13 @@ class _Here:
 
 
 _here = _Here()
+# The current device without the check that CUDA is initialised: there are tensors on it.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _where(dev, stream, *inputs):
     _on_gpu(dev)
-    return _here if stream is None and dev.index == torch.cuda.current_device() else _place(dev, stream, inputs)
+    return _here if stream is None and dev.index == _current_device() else _place(dev, stream, inputs)
 
 
 # The current stream's handle without an object around it, where this torch
