@@ -139,6 +139,25 @@ def test_activations(T, N, act, dtype):
     check(d, act=act, dtype=dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("act", ACTS[1:])
+@pytest.mark.parametrize("T", [5, 300])
+def test_activations_far_out(T, act, dtype):
+    """Sums of any size, where an activation is at its end: a NaN where the formula has one (minus infinity times
+    0), values within 8 * 2^-23 of theirs and their rounding, those below 2^-118 within that (a reciprocal below the
+    normal range may be 0)."""
+    far = [float("inf"), 3.3e38, 2.4e38, 1e30, 1e20, 1e10, 200.0, 90.0, 87.5]
+    d = make(T, 24, 16, 8, scale=0.0)
+    d["bias"] = torch.tensor([s * v for v in far for s in (1.0, -1.0)] + [float("nan"), 0.0, -0.0, -88.5, -104.0, -126.5], device=DEV)
+    got = host(dense_gemm(**d, act=act, out_dtype=dtype))
+    with np.errstate(invalid="ignore"):
+        want = ref.activation(host(d["bias"]), act)
+        off = np.abs(got - want)
+    most = np.abs(want) * (8 * 2.0**-23 + torch.finfo(dtype).eps / 2) + 2.0**-118
+    assert (np.isnan(got) == np.isnan(want)).all()
+    assert ((off <= most) | (got == want) | np.isnan(want)).all(), (got[0], want)
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 40, 8192), (9, 100, 4096), (70, 72, 8192), (260, 300, 4096), (513, 520, 2056)])
 def test_exact_integers(T, N, K):
     """Integers whose sums FP32 holds: bit-equal whatever the order."""
