@@ -72,7 +72,8 @@ __device__ __forceinline__ bool pick_near(const float (&key)[kPer], const float 
   if (__popcll(__ballot(top > kNoKey)) < k) return false;
   const uint32_t t = kth_bound(top, k);
   const float T = __uint_as_float((t & 0x80000000u) ? t ^ 0x80000000u : ~t);
-  const float low = T - (0x1p-20f + 0x1p-21f * fabsf(T));
+  // a finite bound, so that minus infinity (no key) stays out where T is the lowest value
+  const float low = fmaxf(T - (0x1p-20f + 0x1p-21f * fabsf(T)), -0x1.fffffep127f);
   uint64_t sel[kPer];
   int n = 0;
 #pragma unroll

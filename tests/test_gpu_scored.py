@@ -156,6 +156,24 @@ def test_experts_switched_off(scores):
     check(z, b, 6, scores=scores, groups=8, top_groups=2)
 
 
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("E", [32, 256])
+def test_masks_of_the_lowest_value(E, best, scores):
+    """Experts kept out by the lowest finite bias are picked all the same where too few others are there, but those of
+    groups that do not take part are not."""
+    z, b = make(40, E, 6)
+    lowest = torch.finfo(torch.float32).min
+    b[:] = lowest
+    b[E // 2 + 1] = b[3 * E // 4 + 1] = 0.5
+    r = check(z, b, 4, scores=scores, groups=4, top_groups=2, group_best=1)
+    assert (r.ids >= E // 2).all()
+    check(z, b, 4, scores=scores, groups=4, top_groups=2, group_best=best)
+    check(z, b, 4, scores=scores)
+    z[:, 3:] = lowest  # the same in the logits: scores of 0
+    check(z, None, 5, scores=scores, groups=4, top_groups=2, group_best=best)
+
+
 def test_rows_of_minus_infinities():
     """A softmax over nothing has scores and weights of 0, and picks all the same."""
     z = torch.full((40, 32), -float("inf"), device=DEV)
