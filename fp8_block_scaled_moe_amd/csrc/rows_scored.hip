@@ -122,9 +122,10 @@ __device__ __forceinline__ bool best_groups(const moe_route_scored_args& a, int 
   for (int o = 16; o < lanes; o <<= 1) merge(b1, b2, __shfl_xor(b1, o, kWave), __shfl_xor(b2, o, kWave));
   const float value = a.group_best == 2 ? b1 + b2 : b1;
   // groups surely ahead of the lane's own, and those that may be (itself among the latter)
-  const float off = near ? 0x1p-18f + 0x1p-19f * fabsf(value) : 0.f, over = value + off, under = value - off;
+  // (an infinite value, of experts kept out or of a sum past the range, may equal others)
+  const float off = near && fabsf(value) < __builtin_inff() ? 0x1p-18f + 0x1p-19f * fabsf(value) : 0.f, over = value + off, under = value - off;
   const auto ahead = [&](float other, int q) { return other > over || (!near && other == value && q < g); };
-  const auto maybe = [&](float other, int q) { return near ? other > under : ahead(other, q) || q == g; };
+  const auto maybe = [&](float other, int q) { return near ? other >= under : ahead(other, q) || q == g; };
   int sure = 0, may = 0;
   if (G <= lanes) {  // a group's lanes compare it with one other each
     const float other = __shfl(value, sub * lanes, kWave);
@@ -135,7 +136,7 @@ __device__ __forceinline__ bool best_groups(const moe_route_scored_args& a, int 
     sure = __popcll((s >> first) & field);
     may = __popcll((m >> first) & field);
   } else {
-#pragma unroll 2
+#pragma unroll 1
     for (int q = 0; q < G; ++q) {
       const float other = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), q * lanes));
       sure += ahead(other, q) ? 1 : 0;

@@ -157,6 +157,18 @@ def test_experts_switched_off(scores):
 
 
 @pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+def test_groups_with_one_expert_left(scores):
+    """A group's two largest keys add up to minus infinity where all but one of its experts are kept out: such groups go
+    by their index, and what the one expert's key is does not matter."""
+    z, b = make(40, 32, 5)
+    b[8:] = -float("inf")
+    b[20] = 4.0
+    r = check(z, b, 4, scores=scores, groups=4, top_groups=2)
+    assert (r.ids != 20).all()
+    check(z, b, 9, scores=scores, groups=4, top_groups=3)
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("best", [1, 2])
 @pytest.mark.parametrize("E", [32, 256])
 def test_masks_of_the_lowest_value(E, best, scores):
