@@ -137,12 +137,9 @@ __global__ __launch_bounds__(kChunks == 4 ? 512 : 1024) void join_kernel(moe_joi
   }
 }
 
-template <int kChunks>
+template <int kChunks, bool kRouted>
 void launch_join(const moe_join_args& a, int threads, hipStream_t stream) {
-  if (a.norm.k)
-    hipLaunchKernelGGL((join_kernel<kChunks, true>), dim3(a.norm.T), dim3(threads), 0, stream, a);
-  else
-    hipLaunchKernelGGL((join_kernel<kChunks, false>), dim3(a.norm.T), dim3(threads), 0, stream, a);
+  hipLaunchKernelGGL((join_kernel<kChunks, kRouted>), dim3(a.norm.T), dim3(threads), 0, stream, a);
 }
 
 }  // namespace
@@ -172,12 +169,16 @@ extern "C" int moe_join_rmsnorm_quant(const moe_join_args* args, void* stream) {
   // 178 us with one chunk, 158 with two, 164 with four; 3584: 81, 79 and 89). Many plain
   // rows: two up to 4096 columns, four beyond (8,191 x 3584: 73, 68 and 71 us; 4,096 x 8192:
   // 73, 66 and 64).
-  const bool few = a.norm.k == 0 && a.norm.T <= kFewTokens;
-  if (lanes <= (few ? 1024 : 256))
-    launch_join<1>(a, waves(lanes), s);
-  else if (few || a.norm.k > 0 || lanes <= 512)
-    launch_join<2>(a, waves((lanes + 1) / 2), s);
+  const bool few = a.norm.T <= kFewTokens;
+  if (a.norm.k > 0 && lanes <= 256)
+    launch_join<1, true>(a, waves(lanes), s);
+  else if (a.norm.k > 0)
+    launch_join<2, true>(a, waves((lanes + 1) / 2), s);
+  else if (lanes <= (few ? 1024 : 256))
+    launch_join<1, false>(a, waves(lanes), s);
+  else if (few || lanes <= 512)
+    launch_join<2, false>(a, waves((lanes + 1) / 2), s);
   else
-    launch_join<4>(a, waves((lanes + 3) / 4), s);
+    launch_join<4, false>(a, waves((lanes + 3) / 4), s);
   return hipGetLastError() == hipSuccess ? MOE_DECODE_OK : MOE_DECODE_ERR_HIP;
 }
