@@ -9,6 +9,11 @@
 // lie further apart than their errors) and candidates, and only the candidates get
 // exact ones. The groups' largest keys are found through LDS, where a group's experts
 // lie side by side. The grouping of the routes is rows_group.h's.
+//
+// Bound by its instructions: 16,384 tokens x 256 experts in 8 groups, some 520 vector
+// instructions a token, 30.5 us in a graph (19 of them the picks, the two launches of the
+// grouping 10; the logits alone would take 4); without groups 25.0, by softmax 24
+// (128 experts) to 33 (256 in 8 groups). One token: 6 us.
 #include <hip/hip_runtime.h>
 
 #include "../../include/moe_block.h"
@@ -18,20 +23,28 @@
 namespace moe {
 namespace {
 
-// exp(x) for x <= 0 within 2^-47 of its value: 2^(n / 32) by table, where n is the
-// nearest integer to 32 x / ln 2, and five terms for what is left (at most ln 2 / 64;
-// the sixth term is 2^-48.7). The 32 values of the table are the LDS's 64 banks, so
-// lanes that differ in entry differ in bank. Twelve FP64 instructions, where the
+// exp(x) for x <= 0: 2^(n / 32) by table, where n is the nearest integer to 32 x / ln 2,
+// and five or six terms for what is left (at most ln 2 / 64; the sixth term is 2^-48.7,
+// the seventh 2^-58). The 32 values of the table are the LDS's 64 banks, so lanes that
+// differ in entry differ in bank. Twelve or thirteen FP64 instructions, where the
 // library's exponential has twice as many.
 constexpr int kExpParts = 32;
+template <bool kSixth>
 __device__ __forceinline__ double exp_below_0(double x, const double* table) {
   x = fmax(x, -800.0);  // 0 as FP32, and far below any sum's last bit
   const double n = rint(x * (kExpParts * 1.4426950408889634));
   double r = fma(n, -0x1.62e42fee00000p-6, x);  // ln 2 / 32 in two parts
   r = fma(n, -0x1.a39ef35793c76p-38, r);
-  const double p = fma(r, fma(r, fma(r, fma(r, fma(r, 1.0 / 120.0, 1.0 / 24.0), 1.0 / 6.0), 0.5), 1.0), 1.0);
+  const double fifth = kSixth ? fma(r, 1.0 / 720.0, 1.0 / 120.0) : 1.0 / 120.0;
+  const double p = fma(r, fma(r, fma(r, fma(r, fma(r, fifth, 1.0 / 24.0), 1.0 / 6.0), 0.5), 1.0), 1.0);
   const int i = (int)n;
   return ldexp(table[i & (kExpParts - 1)] * p, i >> 5);
+}
+
+// 1 / (1 + exp(-z)) in FP64, rounded to FP32; a NaN stays one.
+__device__ __forceinline__ float sigmoid_of(float z, const double* table) {
+  const double e = exp_below_0<true>(-fabs((double)z), table);
+  return z != z ? z : (float)((z < 0.f ? e : 1.0) / (1.0 + e));
 }
 
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
@@ -47,7 +60,7 @@ __device__ __forceinline__ void softmax_of(const float (&z)[kPer], int E, int la
   double e[kPer], sum = 0.0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    e[j] = lane + kWave * j < E ? exp_below_0((double)z[j] - from, table) : 0.0;
+    e[j] = lane + kWave * j < E ? exp_below_0<false>((double)z[j] - from, table) : 0.0;
     sum += e[j];
     if (j % 2) __builtin_amdgcn_sched_barrier(0);  // all at once, they would take the registers of the logits
   }
@@ -157,7 +170,8 @@ struct Pick {
 template <int kPer, bool kGroups, bool kSoftmax>
 __device__ __forceinline__ Pick pick_exactly(const moe_route_scored_args& sa, int t, int lanes, float* keys, const double* table) {
   const moe_route_args& a = sa.route;
-  const int lane = threadIdx.x & (kWave - 1);
+  int lane = threadIdx.x & (kWave - 1);
+  asm volatile("" : "+v"(lane), "+s"(t));  // as in best_groups
   const bool bf16 = a.logits_dtype == MOE_DTYPE_BF16;
   const size_t row = (size_t)t * a.E;
   int at[kPer];
@@ -169,7 +183,7 @@ __device__ __forceinline__ Pick pick_exactly(const moe_route_scored_args& sa, in
   if (kSoftmax) softmax_of<kPer>(z, a.E, lane, table, score);
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    if (!kSoftmax) score[j] = sigmoid_f32(z[j]);
+    if (!kSoftmax) score[j] = sigmoid_of(z[j], table);
     key[j] = a.bias ? score[j] + a.bias[at[j]] : score[j];
     kv[j] = lane + kWave * j < a.E ? max(ordered_key(key[j]), 1u) : 0u;  // a NaN with every bit set would be 0
     __builtin_amdgcn_sched_barrier(0);
@@ -260,7 +274,7 @@ __device__ __forceinline__ void scored_chunk(const moe_route_scored_args& sa, in
         sure = best_groups<kPer>(sa, lanes, key, !kSoftmax, keys + wave * kPer * kWave, lane, in_groups);
         leave_out(key);
       }
-      const auto exact = [](float v) { return kSoftmax ? v : sigmoid_f32(v); };
+      const auto exact = [&](float v) { return kSoftmax ? v : sigmoid_of(v, table); };
       if (sure) done = pick_near<kPer>(key, z, bias, in, a.k, lane, exact, id, s, total);
     }
     if (done)
