@@ -197,8 +197,8 @@ def join_rmsnorm_quant(residual: Optional[torch.Tensor], gamma: Optional[torch.T
     inplace as in add_rmsnorm_quant; delta and the routed rows (y, pos, weights)
     may not both be absent. post_gamma [D] BF16, None for b as it is, with
     post_eps (None: eps). gate: [T] or [T, 1] FP32 or BF16 (one value for a
-    token), [D] or [1, D] BF16 (for a column), [T, D] BF16, or None. gamma_offset
-    is added to gamma and post_gamma (1.0 where they hold the distance from one)."""
+    token), [D] or [1, D] BF16 (for a column), [T, D] BF16, or None; where T is
+    D, [T, 1] or [1, D] says which. gamma_offset is added to gamma and post_gamma (1.0 where they hold the distance from one)."""
     if quant not in QUANT:
         raise ValueError(f"quant must be one of {list(QUANT)}, got {quant!r}")
     routed = y is not None or pos is not None or weights is not None

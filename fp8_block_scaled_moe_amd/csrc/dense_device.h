@@ -194,7 +194,7 @@ enum DenseShape {
   kDenseHalves,  // 256 x 256, the tiles past whole rounds of the CUs as 128 x 256
 };
 
-void launch_dense_strip(const DenseArgs& a, int shape, hipStream_t stream);// dense_strip.hip
-void launch_dense_tile(const DenseArgs& a, int shape, hipStream_t stream);  // dense_tile.hip
+void launch_dense_strip(const DenseArgs& a, int shape, hipStream_t stream);  // dense_strip.hip
+void launch_dense_tile(const DenseArgs& a, int shape, hipStream_t stream);   // dense_tile.hip
 
 }  // namespace moe

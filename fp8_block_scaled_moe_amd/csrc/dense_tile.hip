@@ -6,8 +6,11 @@
 // instructions. What bounds a large product is power: taking out every wait and barrier
 // of the loop does not change its time, and the 16x16x32 instruction is faster than
 // 32x32x16 at the same rate per cycle (8,192 x 4,096, K = 7168: 326 and 359 us), since it
-// moves its sums half as often. 256 x 256 tiles: 1.47 PFLOP/s at that size; eight waves of 64 x 128 or 128 x 64,
-// two a SIMD (four of 128 x 128 leave a SIMD idle at every wait: 393 us).
+// moves its sums half as often. 256 x 256 tiles: 1.47 PFLOP/s at that size; eight waves of
+// 64 x 128, two a SIMD (four of 128 x 128 leave a SIMD idle at every wait: 393 us). A tile
+// ends in 8 us (8,192 x 4,096, K = 64: 21 us, 67 MB of them stored); workgroups that stay
+// for their next tile and request its blocks before they store were slower (8,192 x 7,168,
+// K = 2048: 197 and 187 us).
 #include <hip/hip_runtime.h>
 
 #include "dense_device.h"
