@@ -5,10 +5,14 @@
 // As rows_norm.hip: one workgroup per token holds the whole row in registers, eight
 // columns a lane and chunk, so every input is read once and every output written once.
 // The second norm's statistics need the first's, so a row crosses the workgroup
-// twice. Both sums of squares are taken in FP64, the way from a block's output to the
-// residual's row in FP32 with four roundings (in FP64, without three of them, it cost
-// 8,191 x 3584 72 us instead of 68: the vector instructions show). Bound by HBM: these
-// at 4.8 TB/s, 4,096 tokens of eight rows of 7168 at 4.6; a large copy runs at 5.2.
+// twice. Both sums of squares are taken in FP64. Both norms round as
+// moe_add_rmsnorm_quant's does (two FP32 products of each value). The residual's row is
+// rounded once: a scale that is a multiple of 2^-15 up to 1 gives FP32 products with a
+// BF16 residual (16 by 8 bits, none below FP32's smallest value), to which the gated
+// value is added by one fused instruction; other scales take both products and their sum
+// through FP64. Bound by HBM: 8,191 x 3584 with a full gate and MXFP8 67 us in a graph, 4.8
+// TB/s, by the first way and 70 by the second; 4,096 tokens of eight rows of 7168 154 us,
+// 4.6; a large copy runs at 5.2.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -99,6 +103,7 @@ __global__ __launch_bounds__(kChunks == 4 ? 512 : 1024) void join_kernel(moe_joi
     }
   }
   const float rstd_post = ja.post_gamma ? (float)row_rstd(sq, part[0], a.D, ja.post_eps) : 1.f;
+  const bool exact = fabsf(ja.residual_scale) <= 1.f && rintf(ja.residual_scale * 0x1p15f) == ja.residual_scale * 0x1p15f;
   sq = 0.0;
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
@@ -110,10 +115,18 @@ __global__ __launch_bounds__(kChunks == 4 ? 512 : 1024) void join_kernel(moe_joi
     unpack8(p[c], pv);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      float by = ja.gate_kind >= MOE_GATE_COLUMN ? uv[i] : gate;
-      if (ja.post_gamma) by *= rstd_post * (pv[i] + ja.gamma_offset);
-      const float v = fmaf(h[c][i], by, rv[i] * ja.residual_scale);
-      h[c][i] = live ? v : 0.f;
+      if (ja.gate_kind < MOE_GATE_COLUMN) uv[i] = gate;
+      if (ja.post_gamma) h[c][i] = (h[c][i] * rstd_post) * (pv[i] + ja.gamma_offset);
+    }
+    if (exact)
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) h[c][i] = fmaf(h[c][i], uv[i], rv[i] * ja.residual_scale);
+    else
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) h[c][i] = (float)fma((double)h[c][i], (double)uv[i], (double)rv[i] * (double)ja.residual_scale);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      h[c][i] = live ? h[c][i] : 0.f;
       sq = fma((double)h[c][i], (double)h[c][i], sq);
     }
     if (a.residual_out && live) *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.residual_out) + row + col) = pack8(h[c]);

@@ -138,11 +138,10 @@ int moe_route_rows_scored(const moe_route_scored_args* a, void* stream);
  *   b = delta[t] + sum_j weights[t, j] * y[pos[t, j]]
  *       summed in FP64 in this order and rounded to FP32 (a position outside
  *       [0, R) adds nothing);
- *   c = rstd(b) * (post_gamma + gamma_offset), or 1 without post_gamma,
+ *   n = (b * rstd(b)) * (post_gamma + gamma_offset) in FP32, or b without post_gamma,
  *       rstd(b) = FP32(1 / sqrt(sum_i b_i^2 / D + post_eps)), the statistics in FP64;
- *   h = b * (gate * c) + residual_scale * residual[t], where gate * c and the
- *       products in it are FP32, the residual's too, and the sum with b's product is
- *       rounded once;
+ *   h = gate * n + residual_scale * residual[t] of exact products, rounded to FP32
+ *       once (by way of FP64 unless residual_scale is a multiple of 2^-15 up to 1);
  *   v = (h * rstd(h)) * (gamma + gamma_offset) in FP32, with eps, or h without gamma;
  *   residual_out[t] = BF16(h), out[t] = BF16(v), q[t] and scale[t] = the 8-bit
  *   form of v (not of BF16(v)).

@@ -94,17 +94,14 @@ def _rstd(h, eps):
 def join_rows(residual, delta, y, pos, weights, *, gamma, eps, post_gamma=None, post_eps=None, gate=None, residual_scale=1.0,
               gamma_offset=0.0):
     """(h, v): the residual row and its normalised form, binary32 values; gate
-    broadcasts against [T, D]. Products and the additions of gamma_offset are
-    rounded to binary32, b's product with its factor only with the sum."""
-    b = np.asarray(sum_rows(None, delta, y, pos, weights), np.float64)
+    broadcasts against [T, D]. Both norms are binary32 steps; the residual row is
+    rounded once, from products that float64 holds exactly."""
+    n = b = np.asarray(sum_rows(None, delta, y, pos, weights), np.float64)
     plus = lambda g: f32(np.asarray(g, np.float64) + float(f32(gamma_offset)))  # noqa: E731
-    factor = np.float64(1.0)
     if post_gamma is not None:
-        factor = f32(_rstd(b, eps if post_eps is None else post_eps) * plus(post_gamma))
-    if gate is not None:
-        factor = f32(factor * np.asarray(gate, np.float64))
-    h = b * factor
+        n = f32(f32(b * _rstd(b, eps if post_eps is None else post_eps)) * plus(post_gamma))
+    h = n * (1.0 if gate is None else np.asarray(gate, np.float64))
     if residual is not None:
-        h = h + f32(np.asarray(residual, np.float64) * float(f32(residual_scale)))
+        h = h + np.asarray(residual, np.float64) * float(f32(residual_scale))
     h = np.asarray(f32(h), np.float64)
     return h, h if gamma is None else f32(f32(h * _rstd(h, eps)) * plus(gamma))
