@@ -134,16 +134,24 @@ __device__ __forceinline__ bool best_groups(const moe_route_scored_args& a, int 
 #pragma unroll 1
   for (int o = 16; o < lanes; o <<= 1) merge(b1, b2, __shfl_xor(b1, o, kWave), __shfl_xor(b2, o, kWave));
   const float value = a.group_best == 2 ? b1 + b2 : b1;
+  // near: a group's exact value lies between `low` and `high`. Its error follows the keys that are added, which may be
+  // far larger than their sum: 2^-21 + 2^-23 (|b1| + |b2|) of theirs and both sums' roundings, half of `off` (an
+  // infinite value, of experts kept out or of a sum past the range, is what it is). Eight times the error sent some
+  // tokens of 4,095 x 896 in 8 groups the exact way: 28.3 us and not 26.
+  float low = value, high = value;
+  if (near && fabsf(value) < __builtin_inff()) {
+    const float off = fmaf(0x1p-21f, a.group_best == 2 ? fabsf(b1) + fabsf(b2) : fabsf(b1), 0x1p-20f);
+    low = value - off;
+    high = value + off;
+  }
   // groups surely ahead of the lane's own, and those that may be (itself among the latter)
-  // (an infinite value, of experts kept out or of a sum past the range, may equal others)
-  const float off = near && fabsf(value) < __builtin_inff() ? 0x1p-18f + 0x1p-19f * fabsf(value) : 0.f, over = value + off, under = value - off;
-  const auto ahead = [&](float other, int q) { return other > over || (!near && other == value && q < g); };
-  const auto maybe = [&](float other, int q) { return near ? other >= under : ahead(other, q) || q == g; };
+  const auto ahead = [&](float other_low, int q) { return other_low > high || (!near && other_low == high && q < g); };
+  const auto maybe = [&](float other_low, float other_high, int q) { return near ? other_high >= low : ahead(other_low, q) || q == g; };
   int sure = 0, may = 0;
   if (G <= lanes) {  // a group's lanes compare it with one other each
-    const float other = __shfl(value, sub * lanes, kWave);
+    const float other = __shfl(low, sub * lanes, kWave), over = near ? __shfl(high, sub * lanes, kWave) : other;
     const bool there = sub < G;
-    const uint64_t s = __ballot(there && ahead(other, sub)), m = __ballot(there && maybe(other, sub));
+    const uint64_t s = __ballot(there && ahead(other, sub)), m = __ballot(there && maybe(other, over, sub));
     const uint64_t field = lanes == kWave ? ~0ull : (1ull << lanes) - 1ull;
     const int first = lane & ~(lanes - 1);
     sure = __popcll((s >> first) & field);
@@ -151,9 +159,10 @@ __device__ __forceinline__ bool best_groups(const moe_route_scored_args& a, int 
   } else {
 #pragma unroll 1
     for (int q = 0; q < G; ++q) {
-      const float other = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), q * lanes));
+      const float other = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(low), q * lanes));
+      const float over = near ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(high), q * lanes)) : other;
       sure += ahead(other, q) ? 1 : 0;
-      may += maybe(other, q) ? 1 : 0;
+      may += maybe(other, over, q) ? 1 : 0;
     }
   }
   in = __ballot(g < G && may <= a.top_groups);
