@@ -49,12 +49,14 @@ __device__ __forceinline__ float sigmoid_of(float z, const double* table) {
 
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
 
-// The softmax of a token's logits, FP32 roundings of FP64 values.
+// The softmax of a token's logits, FP32 roundings of FP64 values. With a NaN or plus
+// infinity among them every exponential counts as 0, and so all are 0 times infinity.
+constexpr uint32_t kNan = 0xFFFFFFFFu;  // the key of a NaN of either sign
 template <int kPer>
 __device__ __forceinline__ void softmax_of(const float (&z)[kPer], int E, int lane, const double* table, float (&s)[kPer]) {
   uint32_t top = 0u;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) top = max(top, lane + kWave * j < E ? ordered_key(z[j]) : 0u);
+  for (int j = 0; j < kPer; ++j) top = max(top, lane + kWave * j >= E ? 0u : z[j] != z[j] ? kNan : ordered_key(z[j]));
   const float m = key_value(wave_max_u32(top));
   const double from = m == -__builtin_inff() ? 0.0 : (double)m;
   double e[kPer], sum = 0.0;
@@ -65,7 +67,7 @@ __device__ __forceinline__ void softmax_of(const float (&z)[kPer], int E, int la
     if (j % 2) __builtin_amdgcn_sched_barrier(0);  // all at once, they would take the registers of the logits
   }
   sum = wave_sum_f64(sum);
-  // of minus infinities alone the sum is E times the exponential of -800: their scores are 0
+  // of minus infinities alone the sum is 0 too: their scores are 0
   const double inv = m == -__builtin_inff() ? 0.0 : 1.0 / sum;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) s[j] = (float)(e[j] * inv);
@@ -175,7 +177,8 @@ struct Pick {
 };
 
 // The picks of token t by the exact keys of all experts: for keys that are NaN or
-// infinite, groups or candidates too close to tell apart.
+// infinite, groups or candidates too close to tell apart. A NaN among the keys shows in
+// all of the token's weights, whether its expert is picked or not.
 template <int kPer, bool kGroups, bool kSoftmax>
 __device__ __forceinline__ Pick pick_exactly(const moe_route_scored_args& sa, int t, int lanes, float* keys, const double* table) {
   const moe_route_args& a = sa.route;
@@ -186,6 +189,7 @@ __device__ __forceinline__ Pick pick_exactly(const moe_route_scored_args& sa, in
   int at[kPer];
   float z[kPer], score[kPer], key[kPer];
   uint32_t kv[kPer];
+  bool nan = false;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) at[j] = min(lane + kWave * j, a.E - 1);
   load_logits<kPer>(bf16 ? (const void*)((const uint16_t*)a.logits + row) : (const void*)((const uint32_t*)a.logits + row), bf16, at, z);
@@ -194,7 +198,8 @@ __device__ __forceinline__ Pick pick_exactly(const moe_route_scored_args& sa, in
   for (int j = 0; j < kPer; ++j) {
     if (!kSoftmax) score[j] = sigmoid_of(z[j], table);
     key[j] = a.bias ? score[j] + a.bias[at[j]] : score[j];
-    kv[j] = lane + kWave * j < a.E ? max(ordered_key(key[j]), 1u) : 0u;  // a NaN with every bit set would be 0
+    kv[j] = lane + kWave * j >= a.E ? 0u : key[j] != key[j] ? kNan : ordered_key(key[j]);
+    nan |= key[j] != key[j];  // lanes past E have the last expert's
     __builtin_amdgcn_sched_barrier(0);
   }
   if (kGroups) {
@@ -205,6 +210,7 @@ __device__ __forceinline__ Pick pick_exactly(const moe_route_scored_args& sa, in
   }
   Pick p;
   pick_top_k<kPer>(kv, score, a.E, a.k, lane, p.id, p.s, p.total);
+  if (__ballot(nan) != 0) p.s = p.total = __builtin_nanf("");
   return p;
 }
 

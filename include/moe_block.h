@@ -113,9 +113,10 @@ size_t moe_dense_gemm_workspace(int32_t T, int32_t N, int32_t K);
  *   weights = (s / total) * routed_scale with renormalise, where total is the
  *           FP32 sum of the picked scores in their order (weights of 0 where it
  *           is 0); otherwise s * routed_scale
- * bias may be NULL. A NaN or an infinity of the logits makes its token's
- * weights NaN or any number, its ids are still k different experts; of minus
- * infinity (an expert switched off) the score is 0.
+ * bias may be NULL. A NaN among a token's logits, of either sign, or in the bias makes
+ * all of its weights NaN, plus infinity its softmax weights; its ids are still k
+ * different experts. Of minus infinity (an expert switched off) the score is 0, of plus
+ * infinity the sigmoid 1.
  * 1 <= groups <= MOE_ROUTE_MAX_GROUPS, a divisor of E; 1 <= top_groups <=
  * groups; group_best 1 or 2, at most E / groups; k <= top_groups * E / groups;
  * all else as in moe_route_rows, moe_route_rows_workspace among it. */
