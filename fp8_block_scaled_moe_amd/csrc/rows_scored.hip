@@ -24,26 +24,23 @@ namespace moe {
 namespace {
 
 // exp(x) for x <= 0: 2^(n / 32) by table, where n is the nearest integer to 32 x / ln 2,
-// and five or six terms for what is left (at most ln 2 / 64; the sixth term is 2^-48.7,
-// the seventh 2^-58). The 32 values of the table are the LDS's 64 banks, so lanes that
-// differ in entry differ in bank. Twelve or thirteen FP64 instructions, where the
-// library's exponential has twice as many.
+// and six terms for what is left (at most ln 2 / 64; the seventh is 2^-58). The 32 values
+// of the table are the LDS's 64 banks, so lanes that differ in entry differ in bank.
+// Thirteen FP64 instructions, where the library's exponential has twice as many.
 constexpr int kExpParts = 32;
-template <bool kSixth>
 __device__ __forceinline__ double exp_below_0(double x, const double* table) {
   x = fmax(x, -800.0);  // 0 as FP32, and far below any sum's last bit
   const double n = rint(x * (kExpParts * 1.4426950408889634));
   double r = fma(n, -0x1.62e42fee00000p-6, x);  // ln 2 / 32 in two parts
   r = fma(n, -0x1.a39ef35793c76p-38, r);
-  const double fifth = kSixth ? fma(r, 1.0 / 720.0, 1.0 / 120.0) : 1.0 / 120.0;
-  const double p = fma(r, fma(r, fma(r, fma(r, fma(r, fifth, 1.0 / 24.0), 1.0 / 6.0), 0.5), 1.0), 1.0);
+  const double p = fma(r, fma(r, fma(r, fma(r, fma(r, fma(r, 1.0 / 720.0, 1.0 / 120.0), 1.0 / 24.0), 1.0 / 6.0), 0.5), 1.0), 1.0);
   const int i = (int)n;
   return ldexp(table[i & (kExpParts - 1)] * p, i >> 5);
 }
 
 // 1 / (1 + exp(-z)) in FP64, rounded to FP32; a NaN stays one.
 __device__ __forceinline__ float sigmoid_of(float z, const double* table) {
-  const double e = exp_below_0<true>(-fabs((double)z), table);
+  const double e = exp_below_0(-fabs((double)z), table);
   return z != z ? z : (float)((z < 0.f ? e : 1.0) / (1.0 + e));
 }
 
@@ -62,7 +59,7 @@ __device__ __forceinline__ void softmax_of(const float (&z)[kPer], int E, int la
   double e[kPer], sum = 0.0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    e[j] = lane + kWave * j < E ? exp_below_0<false>((double)z[j] - from, table) : 0.0;
+    e[j] = lane + kWave * j < E ? exp_below_0((double)z[j] - from, table) : 0.0;
     sum += e[j];
     if (j % 2) __builtin_amdgcn_sched_barrier(0);  // all at once, they would take the registers of the logits
   }
