@@ -35,17 +35,19 @@ __host__ __device__ inline size_t dense_pitch(int N) { return ((size_t)N + 7) / 
 
 // 1 / (1 + exp(-v)) times u, from t = -v log2 e by the hardware's exp2 and reciprocal.
 // kFine (FP32 outputs): what the rounding of t leaves of -v is made up for to first
-// order, so that the error hardly grows with |v|; below -87 the first factor, under
-// 2^-125, counts as 0. For BF16 outputs without: |v| 2^-23 of the value and less, a
-// thousandth of their step, for two thirds of the cycles. A NaN stays one.
+// order, with ln 2 in two parts, so that the error does not grow with |v|: one step of
+// 2^-23 each for the exponential and the reciprocal, half of one for three roundings;
+// below -87 the first factor, under 2^-125, counts as 0. For BF16 outputs without: |v|
+// 2^-23 of the value and less, a thousandth of their step, for two thirds of the cycles.
+// A NaN stays one.
 template <bool kFine>
 __device__ __forceinline__ float times_sigmoid(float v, float u) {
-  constexpr float kLog2e = 0x1.715476p+0f, kLn2 = 0x1.62e43p-1f;
+  constexpr float kLog2e = 0x1.715476p+0f, kLn2 = 0x1.62e43p-1f, kLn2Low = -0x1.05c61p-29f;  // ln 2 in two parts
   if (!kFine) return u * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -kLog2e));
   const bool none = v < -87.f;
   v = clamp_nan(v, -87.f, 87.f);  // neither t nor the exponential is infinite
   const float t = v * -kLog2e, e = __builtin_amdgcn_exp2f(t);
-  return u * (none ? 0.f : __builtin_amdgcn_rcpf(fmaf(e, fmaf(t, -kLn2, -v), 1.f + e)));
+  return u * (none ? 0.f : __builtin_amdgcn_rcpf(fmaf(e, fmaf(t, -kLn2Low, fmaf(t, -kLn2, -v)), 1.f + e)));
 }
 
 template <int kAct, bool kFine>
