@@ -59,10 +59,8 @@ extern "C" {
  * other rows' values, and the same call gives the same bits every time. An
  * infinity or NaN in x or w reaches its own row or column of the output only.
  * Activations are within 4 * 2^-23 of their value (GELU and the tanh form: of
- * |v| where the value is small beside it); values under 2^-118 may be 0; with
- * BF16 outputs SiLU, the sigmoid and the tanh form are another |v| * 2^-23 of
- * their value off (of the exponential's argument), a thousandth of a BF16 step
- * at |v| = 30. ReLU keeps a NaN, an infinity is what the formula makes of it.
+ * |v| where the value is small beside it) in FP32; values under 2^-118 may be 0.
+ * ReLU keeps a NaN, an infinity is what the formula makes of it.
  *   workspace: NULL, or 16-byte aligned device memory of at least
  *   moe_dense_gemm_workspace bytes, with which calls that would leave compute
  *   units idle are split over K (SCRATCH_TOO_SMALL where it is shorter). Its

@@ -37,3 +37,20 @@ def test_fp32_outputs_are_as_near_as_stated(low, high, T, act):
     want = activation(v, act)
     off = np.abs(run(v, act, torch.float32, T) - want) / np.abs(want)
     assert off.max() <= 3.5 * 2.0**-23, f"{off.max() * 2.0**23} at {v[off.argmax()]}"
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("T,odd", [(1, 0), (300, 0), (300, 1)])
+@pytest.mark.parametrize("low,high", [(-80.0, -30.0), (-30.0, -10.0), (-10.0, 10.0)])
+def test_bf16_outputs_are_rounded_from_values_as_near(low, high, T, odd, act):
+    """Values that lie 4.5 to 12 * 2^-23 of themselves beside the middle of two BF16 values round to the right one."""
+    v = np.random.default_rng(int(-low) + odd).uniform(low, high, 4000000).astype(np.float32)
+    want = activation(v, act)
+    below = (np.abs(want).astype(np.float32).view(np.uint32) & 0xFFFF0000).view(np.float32).astype(np.float64)
+    middle = below + np.ldexp(1.0, np.frexp(below)[1] - 9)
+    off = (np.abs(want) - middle) / middle
+    keep = np.flatnonzero((np.abs(off) >= 4.5 * 2.0**-23) & (np.abs(off) <= 12 * 2.0**-23))[: 1200 + odd]
+    right = np.sign(want) * np.where(off > 0, 2 * middle - below, below)
+    got = run(v[keep], act, BF, T)
+    wrong = got != right[keep]
+    assert len(keep) >= 500 and not wrong.any(), f"{int(wrong.sum())} of {len(keep)} values, the first at {v[keep][wrong][0]}"
