@@ -5,12 +5,11 @@
 #include <type_traits>
 
 #include "../../include/moe_block.h"
+#include "dense_plan.h"
 #include "grouped_device.h"
 #include "rows_device.h"
 
 namespace moe {
-
-constexpr int kCus = 256;
 
 // Rows at most this far apart, so that the 256 rows of a tile lie within 2^32 bytes.
 constexpr int64_t kDenseMaxStride = (1 << 23) - 1;
@@ -172,21 +171,6 @@ struct Columns {
 
 // What columns from K on are copied from.
 alignas(16) static __device__ const uint32_t kNothing[4] = {};
-
-// Rows of x by weight rows of a workgroup, and how many workgroups a CU holds.
-enum DenseShape {
-  kDenseStrip4x4,
-  kDenseStrip8x8,
-  kDenseStrip16x16,
-  kDenseStrip16x32,
-  kDenseStrip32x32,
-  kDenseStrip32x64,
-  kDense64x128,
-  kDense128x128,
-  kDense128x128Two,  // two workgroups a CU
-  kDense256x256,
-  kDenseHalves,  // 256 x 256, the tiles past whole rounds of the CUs as 128 x 256
-};
 
 void launch_dense_strip(const DenseArgs& a, int shape, hipStream_t stream);  // dense_strip.hip
 void launch_dense_tile(const DenseArgs& a, int shape, hipStream_t stream);   // dense_tile.hip

@@ -138,8 +138,6 @@ void launch_dense_strip(const DenseArgs& a, int shape, hipStream_t stream) {
   switch (shape) {
     case kDenseStrip4x4:
       return launch<1, 1, 4, 8, 2>(a, stream);
-    case kDenseStrip8x8:
-      return launch<1, 1, 2, 8, 2>(a, stream);
     case kDenseStrip16x16:
       return launch<1, 1, 1, 8, 4>(a, stream);
     case kDenseStrip16x32:
