@@ -6,11 +6,15 @@
 // instructions. What bounds a large product is power: taking out every wait and barrier
 // of the loop does not change its time, and the 16x16x32 instruction is faster than
 // 32x32x16 at the same rate per cycle (8,192 x 4,096, K = 7168: 326 and 359 us), since it
-// moves its sums half as often. 256 x 256 tiles: 1.47 PFLOP/s at that size; eight waves of
+// moves its sums half as often. 256 x 256 tiles: 1.47 PFLOP/s at that size on the same
+// inputs again (1.41 with bias and the tanh form, 1.30 on changing inputs); eight waves of
 // 64 x 128, two a SIMD (four of 128 x 128 leave a SIMD idle at every wait: 393 us). A tile
 // ends in 8 us (8,192 x 4,096, K = 64: 21 us, 67 MB of them stored); workgroups that stay
 // for their next tile and request its blocks before they store were slower (8,192 x 7,168,
-// K = 2048: 197 and 187 us).
+// K = 2048: 197 and 187 us). Short prompts are bound by a block's own chain: at 509 x 7168
+// -> 3584, 64 x 128 tiles, 36 us, a wave has eight matrix instructions between two barriers;
+// of the cycles of a CU the matrix cores are busy for 37%, LDS for 38% (a 16-byte read of a
+// wave takes it four cycles), and the waves wait for 45%.
 #include <hip/hip_runtime.h>
 
 #include "dense_device.h"

@@ -178,9 +178,12 @@ extern "C" int moe_join_rmsnorm_quant(const moe_join_args* args, void* stream) {
   const auto waves = [](int n) { return (n + kWave - 1) / kWave * kWave; };
   // Chunks a lane. Few plain tokens: one, with all of a row's loads on their way at once.
   // Routed rows of more than 2048 columns: two, so that a CU holds two workgroups, of which
-  // one loads while the other is between its barriers (4,096 tokens of eight rows of 7168:
-  // 178 us with one chunk, 158 with two, 164 with four; 3584: 81, 79 and 89). Many plain
-  // rows: two up to 4096 columns, four beyond (8,191 x 3584: 73, 68 and 71 us; 4,096 x 8192:
+  // one loads while the other is between its barriers (eight rows of 7168 for 4,096 tokens:
+  // 173 us with one chunk, 153 with two, 4% more with four; for 512 tokens 25.7 and 21.4 with one
+  // and two; beyond 8192 columns there is one workgroup, and two chunks are faster than four
+  // all the same: 4,096 x 12288 260 and 306, x 16384 349 and 352). A few tokens alone would
+  // take less with one chunk, whose rows come at once: 1 x 7168 8.9 and 9.3, 1 x 4096 6.2
+  // and 7.5, 128 x 7168 11.1 and 11.4. Many plain rows: two up to 4096 columns, four beyond (8,191 x 3584: 73, 68 and 71 us; 4,096 x 8192:
   // 73, 66 and 64).
   const bool few = a.norm.T <= kFewTokens;
   if (a.norm.k > 0 && lanes <= 256)

@@ -10,10 +10,13 @@
 // exact ones. The groups' largest keys are found through LDS, where a group's experts
 // lie side by side. The grouping of the routes is rows_group.h's.
 //
-// Bound by its instructions: 16,384 tokens x 256 experts in 8 groups, some 520 vector
-// instructions a token, 30.5 us in a graph (19 of them the picks, the two launches of the
-// grouping 10; the logits alone would take 4); without groups 25.0, by softmax 24
-// (128 experts) to 33 (256 in 8 groups). One token: 6 us.
+// Bound by its instructions and by a wave's chain of them: 16,384 tokens x 256 experts in
+// 8 groups, some 535 vector instructions a token, 32 us in a graph (21 of them the picks, the
+// two launches of the grouping 10; the logits alone would take 4); without groups 26, by
+// softmax 35. 4,095 x 896 by softmax 27: every wave has one token, its loads, maximum,
+// exponentials, sum, bound and candidates follow each other, and the waves wait for 58% of
+// their cycles; the exponentials in FP64 are 2.5 of it (measured against FP32 ones). One
+// token: 6 us.
 #include <hip/hip_runtime.h>
 
 #include "../../include/moe_block.h"

@@ -4,7 +4,7 @@
  *
  *   moe_dense_gemm          a dense product with bias, activation and residual:
  *                           the router's logits, projections into and out of a
- *                           latent, a dense expert in BF16
+ *                           latent, the products of a dense expert in BF16
  *   moe_route_rows_scored   routing by sigmoid or softmax scores, limited to the
  *                           best groups of experts, and the tokens grouped by
  *                           expert as moe_route_rows does
