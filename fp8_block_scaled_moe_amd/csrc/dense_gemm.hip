@@ -7,7 +7,7 @@ extern "C" {
 
 size_t moe_dense_gemm_workspace(int32_t T, int32_t N, int32_t K) {
   if (T < 1 || N < 1 || K < 1) return 0;
-  const moe::Plan p = moe::dense_plan(T, N, K, true);
+  const moe::DensePlan p = moe::dense_plan(T, N, K, true);
   return p.splits > 1 ? (size_t)p.splits * T * moe::dense_pitch(N) * sizeof(float) : 0;
 }
 
@@ -54,7 +54,7 @@ int moe_dense_gemm(const moe_dense_args* p, void* stream) {
   d.residual_f32 = residual_f32;
   d.vector_io = a.N % 8 == 0 && ldr % 8 == 0 && !misaligned(a.residual, 16);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const Plan plan = dense_plan(a.T, a.N, a.K, a.workspace != nullptr);
+  const DensePlan plan = dense_plan(a.T, a.N, a.K, a.workspace != nullptr);
   d.splits = plan.splits;
   d.partial = static_cast<float*>(a.workspace);
   if (plan.shape < kDense64x128)

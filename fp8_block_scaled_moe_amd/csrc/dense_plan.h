@@ -23,7 +23,7 @@ enum DenseShape {
   kDenseHalves,  // 256 x 256, the tiles past whole rounds of the CUs as 128 x 256
 };
 
-struct Plan {
+struct DensePlan {
   int shape, splits;
   double us;
 };
@@ -38,10 +38,10 @@ struct Plan {
 //   parts of K: a second launch (3 us) and the partial sums written and read.
 // Over 60 sizes drawn from 1 to 16,384 rows the choice was 1.5% slower than the best of
 // all shapes on average, 1.3 times at worst (16,054 rows, K = 88, N = 1).
-inline Plan dense_plan(int T, int N, int K, bool split) {
-  Plan best{kDense64x128, 1, 1e300};
+inline DensePlan dense_plan(int T, int N, int K, bool split) {
+  DensePlan best{kDense64x128, 1, 1e300};
   const auto offer = [&](int shape, int splits, double us) {
-    if (us < best.us) best = Plan{shape, splits, us};
+    if (us < best.us) best = DensePlan{shape, splits, us};
   };
   const auto up = [](double a, double b) { return ceil(a / b); };
   const double cus = kCus, row = (double)K * 2;

@@ -23,7 +23,7 @@ static_assert(moe::kDenseStrip4x4 == 0 && moe::kDenseStrip32x64 == 4 && moe::kDe
 int main() {
   int T, N, K, split;
   while (std::scanf("%d %d %d %d", &T, &N, &K, &split) == 4) {
-    const moe::Plan p = moe::dense_plan(T, N, K, split != 0);
+    const moe::DensePlan p = moe::dense_plan(T, N, K, split != 0);
     std::printf("%d %d\\n", p.shape, p.splits);
   }
 }
